@@ -68,8 +68,28 @@ typedef enum {
 typedef enum {
   DSA_F32 = 0,
   DSA_BF16 = 1,
-  DSA_FP8_E4M3 = 2
+  DSA_FP8_E4M3 = 2,
+  DSA_INT4 = 3         /* mla_dtype only: latent cache in 4 bits, q and out in bf16 */
 } dsa_dtype;
+
+/* Packed latent rows (mla_dtype = DSA_INT4).  A token's row holds its d_c
+ * latent dims in 4 bits and its d_r RoPE dims in bf16:
+ *   bytes [0, d_c/2)      codes, 4-bit two's complement.  Each little-endian
+ *                         32-bit word holds eight dims: nibble i of the low
+ *                         half is dim 2i, nibble i of the high half dim 2i + 1
+ *   then 2*d_r bytes      the RoPE key, bf16, as given
+ *   then d_c/16 bytes     one scale per 16 consecutive latent dims, an unsigned
+ *                         8-bit float of 5 exponent and 3 mantissa bits: the
+ *                         fp16 number whose bit pattern is the byte << 7
+ *   then zeros up to a multiple of 16 bytes
+ * (416 bytes for d_c = 512, d_r = 64; dsa_latent_row_bytes).  The value of a
+ * dim is code * scale: at most 4 + 4 significant bits, so it is exact in bf16.
+ * The writers choose, per 16 dims c with a = max |c|,
+ *   scale = the nearest 8-bit scale to fl32(a / 7) (ties to even, at most 61440)
+ *   code  = clamp(round(fl32(c / scale)), -7, 7)   (ties to even; 0 when scale = 0)
+ * and never write the code -8 or a scale byte above 0xF7 (readers take both).
+ * The RoPE key stays in bf16: it is not normalised like the latent, positions
+ * turn on its exact phases, and it is 128 of the 416 bytes. */
 
 /* Which kernels to run.  AUTO picks the tensor-core kernels (tcgen05) for the
  * FP8 indexer with H_I*group <= 256, d_I = 128, and for bf16 MLA with
@@ -97,7 +117,8 @@ typedef struct {
   int32_t d_r;           /* decoupled RoPE key width                    */
   int32_t topk;          /* k, 1 <= k <= 2048                           */
   dsa_dtype idx_dtype;   /* DSA_FP8_E4M3 (scales required) or DSA_F32   */
-  dsa_dtype mla_dtype;   /* DSA_BF16 or DSA_F32                         */
+  dsa_dtype mla_dtype;   /* DSA_BF16, DSA_F32 or DSA_INT4 (then d_c is a
+                            multiple of 32, at most 512, and d_r of 8)  */
   float sm_scale;        /* softmax scale, e.g. 1/sqrt(d_c + d_r)       */
   dsa_algo algo;
 } dsa_dims;
@@ -122,7 +143,8 @@ typedef struct {
  *                                * page_size + s % page_size
  *   contiguous:                  seq_start[b] + s   (seq_start NULL: s)        */
 typedef struct {
-  const void* latent;         /* [num_tokens, d_c + d_r] bf16 | f32, row-major  */
+  const void* latent;         /* [num_tokens, d_c + d_r] bf16 | f32, row-major,
+                                 or packed rows of dsa_latent_row_bytes (DSA_INT4) */
   const void* idx_k;          /* [num_tokens, d_idx] e4m3 | f32, row-major      */
   const float* idx_k_scale;   /* [num_tokens] (required for e4m3, else NULL)     */
   const int32_t* seq_start;   /* [num_seqs] or NULL (contiguous layout)          */
@@ -141,7 +163,9 @@ typedef enum {
   DSA_OP_FORWARD = 4,
   DSA_OP_CACHE_APPEND = 5,
   DSA_OP_INDEXER_KL = 6,
-  DSA_OP_INDEXER_BACKWARD = 7
+  DSA_OP_INDEXER_BACKWARD = 7,
+  DSA_OP_CACHE_READ = 8,
+  DSA_OP_BATCH_PLAN = 9
 } dsa_op;
 
 /* Human-readable name of a status code (static storage). */
@@ -156,8 +180,13 @@ int32_t dsa_version(void);
 /* Bytes of workspace `op` needs for these dimensions and rows (host only; it
  * reads the current device's SM count, which sets the decode key splits, and
  * uses 148 when no device is present).  Returns 0 for invalid arguments.
- * DSA_OP_CACHE_APPEND needs only the status block; `rows` may be NULL for it. */
+ * DSA_OP_CACHE_APPEND and DSA_OP_CACHE_READ need only the status block; `rows`
+ * may be NULL for them, and `dims` too for DSA_OP_BATCH_PLAN. */
 size_t dsa_workspace_size(const dsa_dims* dims, const dsa_rows* rows, dsa_op op);
+
+/* Bytes of one token's row of the latent cache for these dimensions (host only):
+ * (d_c + d_r) elements, or a packed row for DSA_INT4.  0 for invalid dimensions. */
+size_t dsa_latent_row_bytes(const dsa_dims* dims);
 
 /* Zero the workspace `ws` (ws_bytes bytes, async on stream): the device status
  * word at its head and, for dsa_decode_step and dsa_forward, the per-row
@@ -190,6 +219,9 @@ dsa_status dsa_read_device_status(void* ws, dsa_stream_t stream, int32_t* status
 #define DSA_KERNEL_OUT_PROJ     0x80u   /* tcgen05 output projection GEMM */
 #define DSA_KERNEL_OUT_PROJ_REDUCE 0x100u   /* split-K sum of the W_out product */
 #define DSA_KERNEL_WARMUP       0x200u   /* indexer warm-up: KL and backward kernels */
+#define DSA_KERNEL_MLA_INT4_TC  0x400u   /* tcgen05 sparse MLA over packed 4-bit rows */
+#define DSA_KERNEL_CACHE_READ   0x800u   /* gather + dequantise of cached tokens */
+#define DSA_KERNEL_BATCH_PLAN   0x1000u  /* block table, slot map and row map of a step */
 
 /* Synchronise `stream`, return the kernel trace of `ws` in *mask_out and clear it. */
 dsa_status dsa_read_kernel_trace(void* ws, dsa_stream_t stream, uint32_t* mask_out);
@@ -255,7 +287,7 @@ dsa_status dsa_topk(const dsa_dims* dims, const dsa_rows* rows, const float* sco
                     dsa_stream_t stream);
 
 /* Stage 3: sparse absorbed MLA over the selected rows.
- *   q   [T, H, d_c + d_r] bf16 | f32
+ *   q   [T, H, d_c + d_r] bf16 (DSA_BF16, DSA_INT4) | f32
  *   idx [T, topk] int32 logical positions (entries < 0 are skipped; entries
  *       >= klen[t] are a caller error and are read as given)
  *   out [T, H, d_c] bf16 | f32 (same dtype as q)
@@ -326,6 +358,10 @@ dsa_status dsa_forward(const dsa_dims* dims, const dsa_rows* rows, const dsa_cac
  *   idx_k_scale[row] = s
  *   latent[row]      = latent_new[n, :]   (bit copy)
  * With idx_dtype = DSA_F32 the key is copied and idx_k_scale is not used.
+ * With mla_dtype = DSA_INT4 latent_new is bf16 and latent[row] is the packed row
+ * defined above; a token with an infinity or NaN among its latent dims is not
+ * written and is recorded as DSA_ERR_INVALID_ARG like one in the key (the RoPE
+ * dims are a bit copy).
  *   tok_seq, tok_pos [n_new] int32, device
  *   k_new      [n_new, d_idx] fp32, device, 16-byte aligned; d_idx <= 512
  *   latent_new [n_new, d_c + d_r] in mla_dtype, device, 16-byte aligned
@@ -354,6 +390,85 @@ dsa_status dsa_cache_append(const dsa_dims* dims, const dsa_cache* cache, int32_
                             const int32_t* tok_seq, const int32_t* tok_pos,
                             const float* k_new, const void* latent_new,
                             void* ws, size_t ws_bytes, dsa_stream_t stream);
+
+/* dsa_cache_append by slot: token n goes to physical cache row slot[n] (as
+ * dsa_batch_plan gives it), the same quantisation and checks.  slot[n] < 0 skips
+ * token n without an error, so that a batch may be padded; slot[n] >= num_tokens
+ * is not written and is recorded as DSA_ERR_OUT_OF_RANGE with detail n.  Slots of
+ * one call are distinct.  k_new or latent_new may be NULL: that cache is left as
+ * it is (and need not be given).
+ *   slot [n] int64, device */
+dsa_status dsa_cache_append_slots(const dsa_dims* dims, const dsa_cache* cache, int32_t n,
+                                  const int64_t* slot, const float* k_new, const void* latent_new,
+                                  void* ws, size_t ws_bytes, dsa_stream_t stream);
+
+/* Reads cached tokens back as the values they stand for: the gather with
+ * dequantisation that an un-absorbed prefill over a cached context, or the move
+ * of a sequence to another cache, starts with.
+ *   slot       [n] int64, device: physical cache rows, in any order, repeats allowed
+ *   k_out      [n, d_idx] fp32 out: fl32(e4m3 code * scale), or the fp32 key; NULL: not read
+ *   latent_out [n, d_c + d_r] out, f32 for DSA_F32 and bf16 otherwise; NULL: not read.
+ *              Exact: DSA_INT4 values have at most 8 significant bits.
+ * Rows of slot[n] < 0 are left as they are; slot[n] >= num_tokens too, and is
+ * recorded as DSA_ERR_OUT_OF_RANGE with detail n.  Outputs 16-byte aligned.
+ * ws: dsa_workspace_size(dims, NULL, DSA_OP_CACHE_READ) bytes (the status block). */
+dsa_status dsa_cache_read(const dsa_dims* dims, const dsa_cache* cache, int32_t n,
+                          const int64_t* slot, float* k_out, void* latent_out,
+                          void* ws, size_t ws_bytes, dsa_stream_t stream);
+
+/* Batch plan: the block table, slot map and row map of one step, built on the GPU
+ * from the requests' lengths, with the pages taken from and handed back to a
+ * free list.  All pointers device memory.  B = cache->num_seqs, P = page_size. */
+typedef struct {
+  const int32_t* seq_len;    /* [B] tokens cached before the step                       */
+  const int32_t* n_new;      /* [B] tokens to add (0: none)                             */
+  const int32_t* release;    /* [B] nonzero: the request is done, its pages go back
+                                (n_new must be 0 there); NULL: none                     */
+  int32_t* seq_len_out;      /* [B] tokens cached after it (may be seq_len)             */
+  const int32_t* free_count; /* [1] entries of free_pages in use (paged only)           */
+  int32_t* free_count_out;   /* [1] after the step (may be free_count; paged only)      */
+  int32_t* free_pages;       /* [free_capacity] stack of free page ids (paged only)     */
+  int32_t free_capacity;     /* at least the number of pages of the cache               */
+  int32_t max_tokens;        /* rows of the outputs below                               */
+  int32_t* tok_start;        /* [B + 1] first row of each request; [B]: rows in use     */
+  int32_t* row_seq;          /* [max_tokens] request of the row                         */
+  int32_t* row_klen;         /* [max_tokens] keys the row sees: its position + 1        */
+  int32_t* tok_pos;          /* [max_tokens] logical position of the row's token        */
+  int64_t* slot;             /* [max_tokens] physical cache row of the token            */
+  int32_t* totals;           /* [4] rows in use, pages taken, requests refused,
+                                pages handed back                                       */
+} dsa_plan;
+
+/* Requests with release set hand back their ceil(seq_len / P) pages, in request
+ * and page order on top of the free list, and end with length 0.  Every other
+ * request b needs need[b] = ceil((seq_len + n_new)/P) - ceil(seq_len/P) pages and
+ * n_new[b] rows.  It is planned when
+ *     need[b] = 0   or  need[0] + ... + need[b]  <= pages on the free list, and
+ *     n_new[b] = 0  or  n_new[0] + ... + n_new[b] <= max_tokens,
+ * sums over all requests that could run, planned or not.  A request that is not
+ * planned keeps its length, gets no rows and counts as refused; that is no error.
+ * Pages are popped from the top of the list in request and page order; their ids
+ * are written into the request's row of cache->block_table (written here; the
+ * descriptor is shared with the calls that read it), and seq_len_out = seq_len +
+ * n_new.  Rows are packed in request order.  Row t of request b, j-th of its
+ * rows: tok_pos = seq_len[b] + j, row_klen = tok_pos + 1, slot = page * P +
+ * tok_pos % P.  Rows behind the last one get tok_pos = slot = -1, row_klen = 0 and
+ * the row_seq of the last planned row (0 if none), so that dsa_rows of max_tokens
+ * rows and dsa_cache_append_slots may run on the padded batch: a captured graph
+ * needs no host decision.  With a contiguous cache (block_table NULL) there are no
+ * pages: slot = seq_start[b] + tok_pos, and a request beyond num_tokens is refused.
+ * Free-list entries at and above free_count_out are unspecified where pages were
+ * handed back, and as they were elsewhere.
+ * Device errors (the lowest such request is the detail): DSA_ERR_INVALID_ARG for a
+ * negative length or count, a seq_len beyond the block table, a release with
+ * n_new != 0 (such a request is left as it is), or a free count outside
+ * [0, free_capacity] (taken as 0); DSA_ERR_OUT_OF_RANGE for a
+ * request longer than its row of the block table (refused), and for a page id
+ * outside the cache, whose block-table entry and slots become -1.
+ * B <= 16384 and B * max_pages_per_seq < 2^31.  Deterministic; one kernel.
+ * ws: dsa_workspace_size(NULL, NULL, DSA_OP_BATCH_PLAN) bytes (the status block). */
+dsa_status dsa_batch_plan(const dsa_cache* cache, const dsa_plan* plan, void* ws, size_t ws_bytes,
+                          dsa_stream_t stream);
 
 /* Output projection: the two GEMMs after the path that complete u_t
  * ("DeepSeek Sparse Attention DSA Architecture Guide", section "Stage 2:

@@ -12,16 +12,18 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdsa.so")
 
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_CUDA = 0, 1, 2, 3
 DSA_ERR_OUT_OF_RANGE, DSA_ERR_TIMEOUT, DSA_ERR_WORKSPACE = 4, 5, 6
-DSA_F32, DSA_BF16, DSA_FP8_E4M3 = 0, 1, 2
+DSA_F32, DSA_BF16, DSA_FP8_E4M3, DSA_INT4 = 0, 1, 2, 3
 DSA_ALGO_AUTO, DSA_ALGO_SIMT, DSA_ALGO_STAGED = 0, 1, 2
 DSA_OP_INDEXER, DSA_OP_TOPK, DSA_OP_SPARSE_MLA, DSA_OP_DECODE_STEP, DSA_OP_FORWARD = range(5)
 DSA_OP_CACHE_APPEND = 5
 DSA_OP_INDEXER_KL, DSA_OP_INDEXER_BACKWARD = 6, 7
+DSA_OP_CACHE_READ, DSA_OP_BATCH_PLAN = 8, 9
 DSA_KERNEL_INDEXER_SIMT, DSA_KERNEL_INDEXER_TC, DSA_KERNEL_TOPK = 0x01, 0x02, 0x04
 DSA_KERNEL_MLA_SIMT, DSA_KERNEL_MLA_TC, DSA_KERNEL_MLA_COMBINE = 0x08, 0x10, 0x20
 DSA_KERNEL_CACHE_APPEND = 0x40
 DSA_KERNEL_OUT_PROJ, DSA_KERNEL_OUT_PROJ_REDUCE = 0x80, 0x100
 DSA_KERNEL_WARMUP = 0x200
+DSA_KERNEL_MLA_INT4_TC, DSA_KERNEL_CACHE_READ, DSA_KERNEL_BATCH_PLAN = 0x400, 0x800, 0x1000
 DSA_FAULT_INDEXER_ACC_RELEASE = 0x1
 
 
@@ -44,6 +46,16 @@ class dsa_cache(ctypes.Structure):
                 ("block_table", ctypes.c_void_p), ("page_size", ctypes.c_int32),
                 ("max_pages_per_seq", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
                 ("num_tokens", ctypes.c_int64)]
+
+
+class dsa_plan(ctypes.Structure):
+    _fields_ = [("seq_len", ctypes.c_void_p), ("n_new", ctypes.c_void_p), ("release", ctypes.c_void_p),
+                ("seq_len_out", ctypes.c_void_p), ("free_count", ctypes.c_void_p),
+                ("free_count_out", ctypes.c_void_p), ("free_pages", ctypes.c_void_p),
+                ("free_capacity", ctypes.c_int32), ("max_tokens", ctypes.c_int32),
+                ("tok_start", ctypes.c_void_p), ("row_seq", ctypes.c_void_p),
+                ("row_klen", ctypes.c_void_p), ("tok_pos", ctypes.c_void_p),
+                ("slot", ctypes.c_void_p), ("totals", ctypes.c_void_p)]
 
 
 class dsa_proj_dims(ctypes.Structure):
@@ -74,6 +86,11 @@ _SIGS = {
                                    ctypes.c_size_t, _P]),
     "dsa_cache_append": (ctypes.c_int, [_P, _P, ctypes.c_int32, _P, _P, _P, _P, _P,
                                         ctypes.c_size_t, _P]),
+    "dsa_latent_row_bytes": (ctypes.c_size_t, [_P]),
+    "dsa_cache_append_slots": (ctypes.c_int, [_P, _P, ctypes.c_int32, _P, _P, _P, _P, ctypes.c_size_t,
+                                              _P]),
+    "dsa_cache_read": (ctypes.c_int, [_P, _P, ctypes.c_int32, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "dsa_batch_plan": (ctypes.c_int, [_P, _P, _P, ctypes.c_size_t, _P]),
     "dsa_indexer_kl": (ctypes.c_int, [_P, _P, ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_int64,
                                       _P, _P, ctypes.c_size_t, _P]),
     "dsa_indexer_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_int64, _P, _P, _P,
@@ -188,6 +205,24 @@ def dsa_cache_append(dims, cache, n_new, tok_seq, tok_pos, k_new, latent_new, ws
                      stream, check=True):
     return _call("dsa_cache_append", _ref(dims), _ref(cache), n_new, tok_seq, tok_pos, k_new,
                  latent_new, ws, ws_bytes, stream, check=check)
+
+
+def dsa_latent_row_bytes(dims) -> int:
+    return LIB.dsa_latent_row_bytes(_ref(dims))
+
+
+def dsa_cache_append_slots(dims, cache, n, slot, k_new, latent_new, ws, ws_bytes, stream, check=True):
+    return _call("dsa_cache_append_slots", _ref(dims), _ref(cache), n, slot, k_new, latent_new, ws,
+                 ws_bytes, stream, check=check)
+
+
+def dsa_cache_read(dims, cache, n, slot, k_out, latent_out, ws, ws_bytes, stream, check=True):
+    return _call("dsa_cache_read", _ref(dims), _ref(cache), n, slot, k_out, latent_out, ws, ws_bytes,
+                 stream, check=check)
+
+
+def dsa_batch_plan(cache, plan, ws, ws_bytes, stream, check=True):
+    return _call("dsa_batch_plan", _ref(cache), _ref(plan), ws, ws_bytes, stream, check=check)
 
 
 def dsa_output_projection_ws_size(dims, num_rows) -> int:

@@ -7,6 +7,7 @@
 #include <mutex>
 #include <unordered_map>
 
+#include "dsa_int4.cuh"
 #include "dsa_kernels.cuh"
 
 namespace dsa {
@@ -89,12 +90,17 @@ dsa_status check_dims(const dsa_dims* d) {
             "non-positive dimension");
   CHECK_ARG(d->topk >= 1 && d->topk <= 2048, "topk %d outside [1, 2048]", d->topk);
   CHECK_ARG(d->idx_dtype == DSA_FP8_E4M3 || d->idx_dtype == DSA_F32, "idx_dtype must be e4m3 or f32");
-  CHECK_ARG(d->mla_dtype == DSA_BF16 || d->mla_dtype == DSA_F32, "mla_dtype must be bf16 or f32");
+  CHECK_ARG(d->mla_dtype == DSA_BF16 || d->mla_dtype == DSA_F32 || d->mla_dtype == DSA_INT4,
+            "mla_dtype must be bf16, f32 or int4");
   CHECK_ARG(d->algo == DSA_ALGO_AUTO || d->algo == DSA_ALGO_SIMT || d->algo == DSA_ALGO_STAGED,
             "unknown algo");
   CHECK_ARG(d->sm_scale > 0.f, "sm_scale must be > 0");
   if (d->d_idx % 4 != 0 || (d->d_c + d->d_r) % 8 != 0) {
     set_error("d_idx must be a multiple of 4 and d_c + d_r a multiple of 8");
+    return DSA_ERR_UNSUPPORTED;
+  }
+  if (d->mla_dtype == DSA_INT4 && (d->d_c % 32 != 0 || d->d_c > 512 || d->d_r % 8 != 0)) {
+    set_error("int4 latents take d_c %% 32 == 0, d_c <= 512 and d_r %% 8 == 0");
     return DSA_ERR_UNSUPPORTED;
   }
   return DSA_OK;
@@ -145,6 +151,14 @@ dsa_status check_proj(const dsa_proj_dims* d) {
 size_t proj_partial_bytes(const dsa_proj_dims* d, int32_t T) {
   const int splits = out_proj_splits(T, d->d_model, d->n_heads * d->d_v / 64);
   return splits > 1 ? align_up((size_t)splits * (size_t)T * (size_t)d->d_model * sizeof(float)) : 0;
+}
+
+// Bytes of one token's row of the latent cache, and of the same row in the type
+// that queries, outputs and new tokens have (bf16 beside int4 latents).
+size_t mla_elem(const dsa_dims* d) { return d->mla_dtype == DSA_F32 ? 4 : 2; }
+size_t latent_value_bytes(const dsa_dims* d) { return (size_t)(d->d_c + d->d_r) * mla_elem(d); }
+size_t latent_row_bytes(const dsa_dims* d) {
+  return d->mla_dtype == DSA_INT4 ? (size_t)int4_row(d->d_c, d->d_r).bytes : latent_value_bytes(d);
 }
 
 CacheMap make_map(const dsa_cache* c) {
@@ -239,6 +253,24 @@ dsa_status check_ws(void* ws, size_t ws_bytes, size_t need) {
 
 uint8_t* at(void* ws, size_t off) { return static_cast<uint8_t*>(ws) + off; }
 
+// The part of the append's arguments that both forms of the call share.
+void append_caches(AppendArgs& a, const dsa_dims* d, const dsa_cache* c, void* ws) {
+  a.d_idx = d->d_idx;
+  a.d_c = d->d_c;
+  a.d_r = d->d_r;
+  a.int4 = d->mla_dtype == DSA_INT4;
+  a.latent_row_bytes = (int)latent_row_bytes(d);
+  a.latent_new_row_bytes = (int)latent_value_bytes(d);
+  a.idx_dtype = d->idx_dtype;
+  // the caches are written here; the descriptor is shared with the read-only calls
+  a.idx_k = const_cast<void*>(c->idx_k);
+  a.idx_k_scale = const_cast<float*>(c->idx_k_scale);
+  a.latent = const_cast<void*>(c->latent);
+  a.map = make_map(c);
+  a.num_seqs = c->num_seqs;
+  a.status = reinterpret_cast<DeviceStatus*>(ws);
+}
+
 IndexerArgs indexer_args(const dsa_dims* d, const dsa_rows* r, const dsa_cache* c,
                          const void* q_idx, const float* q_scale, const float* w, float* scores,
                          int64_t ld, void* ws, const WsPlan& p) {
@@ -331,6 +363,7 @@ MlaArgs mla_args(const dsa_dims* d, const dsa_rows* r, const dsa_cache* c, const
   a.idx = idx;
   a.latent = c->latent;
   a.map = make_map(c);
+  a.num_seqs = c->num_seqs;
   a.out = out;
   a.lse = lse;
   a.status = reinterpret_cast<DeviceStatus*>(ws);
@@ -407,11 +440,16 @@ const char* dsa_last_error(void) { return g_err; }
 int32_t dsa_version(void) { return 100; }
 
 size_t dsa_workspace_size(const dsa_dims* dims, const dsa_rows* rows, dsa_op op) {
-  if (op == DSA_OP_CACHE_APPEND) return check_dims(dims) == DSA_OK ? kStatusBytes : 0;
-  if (op == DSA_OP_INDEXER_KL) return kStatusBytes;
+  if (op == DSA_OP_CACHE_APPEND || op == DSA_OP_CACHE_READ)
+    return check_dims(dims) == DSA_OK ? kStatusBytes : 0;
+  if (op == DSA_OP_INDEXER_KL || op == DSA_OP_BATCH_PLAN) return kStatusBytes;
   if (check_dims(dims) != DSA_OK || check_rows(rows) != DSA_OK) return 0;
   if (op < DSA_OP_INDEXER || op > DSA_OP_INDEXER_BACKWARD || op == DSA_OP_CACHE_APPEND) return 0;
   return plan(dims, rows, op).total;
+}
+
+size_t dsa_latent_row_bytes(const dsa_dims* dims) {
+  return check_dims(dims) == DSA_OK ? latent_row_bytes(dims) : 0;
 }
 
 dsa_status dsa_workspace_init(void* ws, size_t ws_bytes, dsa_stream_t stream) {
@@ -660,7 +698,7 @@ dsa_status dsa_forward(const dsa_dims* dims, const dsa_rows* rows, const dsa_cac
   const int H_I = dims->n_idx_heads, D_I = dims->d_idx, H = dims->n_heads;
   const int DQK = dims->d_c + dims->d_r;
   const size_t qi_el = dims->idx_dtype == DSA_FP8_E4M3 ? 1 : 4;
-  const size_t mla_el = dims->mla_dtype == DSA_BF16 ? 2 : 4;
+  const size_t mla_el = mla_elem(dims);
   float* scores = reinterpret_cast<float*>(at(ws, p.scores));
   int32_t* idx_ws = reinterpret_cast<int32_t*>(at(ws, p.idx));
   bool used_hist = false;
@@ -728,17 +766,108 @@ dsa_status dsa_cache_append(const dsa_dims* dims, const dsa_cache* cache, int32_
   a.tok_pos = tok_pos;
   a.k_new = k_new;
   a.latent_new = latent_new;
-  a.d_idx = dims->d_idx;
-  a.latent_row_bytes = (dims->d_c + dims->d_r) * (dims->mla_dtype == DSA_BF16 ? 2 : 4);
-  a.idx_dtype = dims->idx_dtype;
-  // the caches are written here; the descriptor is shared with the read-only calls
-  a.idx_k = const_cast<void*>(cache->idx_k);
-  a.idx_k_scale = const_cast<float*>(cache->idx_k_scale);
-  a.latent = const_cast<void*>(cache->latent);
-  a.map = make_map(cache);
-  a.num_seqs = cache->num_seqs;
-  a.status = reinterpret_cast<DeviceStatus*>(ws);
+  append_caches(a, dims, cache, ws);
   return launch_cache_append(a, (cudaStream_t)stream);
+}
+
+dsa_status dsa_cache_append_slots(const dsa_dims* dims, const dsa_cache* cache, int32_t n,
+                                  const int64_t* slot, const float* k_new, const void* latent_new,
+                                  void* ws, size_t ws_bytes, dsa_stream_t stream) {
+  dsa_status st;
+  if ((st = check_dims(dims)) != DSA_OK) return st;
+  if ((st = check_cache(cache, dims, k_new != nullptr, latent_new != nullptr)) != DSA_OK) return st;
+  CHECK_ARG(n >= 0, "n must be >= 0");
+  if ((st = check_ws(ws, ws_bytes, kStatusBytes)) != DSA_OK) return st;
+  if (k_new != nullptr && dims->d_idx > cache_append_max_d_idx()) {
+    set_error("cache append takes d_idx <= %d", cache_append_max_d_idx());
+    return DSA_ERR_UNSUPPORTED;
+  }
+  if (n == 0) return DSA_OK;
+  CHECK_ARG(slot != nullptr && aligned(slot, 8), "slot must be non-NULL and 8-byte aligned");
+  CHECK_ARG(k_new != nullptr || latent_new != nullptr, "k_new and latent_new are both NULL");
+  CHECK_ARG(aligned(k_new, 16) && aligned(latent_new, 16), "k_new and latent_new must be 16-byte aligned");
+  AppendArgs a{};
+  a.n_new = n;
+  a.slot = slot;
+  a.k_new = k_new;
+  a.latent_new = latent_new;
+  append_caches(a, dims, cache, ws);
+  return launch_cache_append(a, (cudaStream_t)stream);
+}
+
+dsa_status dsa_cache_read(const dsa_dims* dims, const dsa_cache* cache, int32_t n, const int64_t* slot,
+                          float* k_out, void* latent_out, void* ws, size_t ws_bytes, dsa_stream_t stream) {
+  dsa_status st;
+  if ((st = check_dims(dims)) != DSA_OK) return st;
+  if ((st = check_cache(cache, dims, k_out != nullptr, latent_out != nullptr)) != DSA_OK) return st;
+  CHECK_ARG(n >= 0, "n must be >= 0");
+  if ((st = check_ws(ws, ws_bytes, kStatusBytes)) != DSA_OK) return st;
+  if (n == 0) return DSA_OK;
+  CHECK_ARG(slot != nullptr && aligned(slot, 8), "slot must be non-NULL and 8-byte aligned");
+  CHECK_ARG(k_out != nullptr || latent_out != nullptr, "k_out and latent_out are both NULL");
+  CHECK_ARG(aligned(k_out, 16) && aligned(latent_out, 16), "k_out and latent_out must be 16-byte aligned");
+  ReadArgs a{};
+  a.n = n;
+  a.slot = slot;
+  a.idx_k = cache->idx_k;
+  a.idx_k_scale = cache->idx_k_scale;
+  a.latent = cache->latent;
+  a.k_out = k_out;
+  a.latent_out = latent_out;
+  a.d_idx = dims->d_idx;
+  a.d_c = dims->d_c;
+  a.d_r = dims->d_r;
+  a.latent_row_bytes = (int)latent_row_bytes(dims);
+  a.idx_dtype = dims->idx_dtype;
+  a.int4 = dims->mla_dtype == DSA_INT4;
+  a.num_tokens = cache->num_tokens;
+  a.status = reinterpret_cast<DeviceStatus*>(ws);
+  return launch_cache_read(a, (cudaStream_t)stream);
+}
+
+dsa_status dsa_batch_plan(const dsa_cache* cache, const dsa_plan* plan, void* ws, size_t ws_bytes,
+                          dsa_stream_t stream) {
+  dsa_status st;
+  CHECK_ARG(cache != nullptr && plan != nullptr, "cache or plan is NULL");
+  CHECK_ARG(cache->num_seqs > 0 && cache->num_tokens >= 0, "cache needs num_seqs > 0");
+  CHECK_ARG(plan->max_tokens >= 0, "max_tokens must be >= 0");
+  CHECK_ARG(plan->seq_len && plan->n_new && plan->seq_len_out && plan->tok_start && plan->totals,
+            "seq_len / n_new / seq_len_out / tok_start / totals is NULL");
+  CHECK_ARG(plan->max_tokens == 0 || (plan->row_seq && plan->row_klen && plan->tok_pos && plan->slot),
+            "row_seq / row_klen / tok_pos / slot is NULL");
+  CHECK_ARG(aligned(plan->slot, 8), "slot must be 8-byte aligned");
+  if (cache->num_seqs > batch_plan_max_seqs()) {
+    set_error("batch plan takes num_seqs <= %d", batch_plan_max_seqs());
+    return DSA_ERR_UNSUPPORTED;
+  }
+  PlanArgs a{};
+  a.p = *plan;
+  a.num_seqs = cache->num_seqs;
+  a.num_tokens = cache->num_tokens;
+  a.page_size = 1;
+  if (cache->block_table) {
+    CHECK_ARG(cache->page_size > 0 && cache->max_pages_per_seq > 0, "paged cache needs page_size > 0");
+    CHECK_ARG(cache->num_tokens % cache->page_size == 0, "num_tokens must be num_pages * page_size");
+    CHECK_ARG(cache->num_tokens / cache->page_size <= INT32_MAX, "too many pages");
+    CHECK_ARG(plan->free_count && plan->free_count_out && plan->free_pages,
+              "free_count / free_count_out / free_pages is NULL");
+    CHECK_ARG(plan->free_capacity >= cache->num_tokens / cache->page_size,
+              "free_capacity must hold every page of the cache");
+    if ((int64_t)cache->num_seqs * cache->max_pages_per_seq > INT32_MAX) {
+      set_error("batch plan takes num_seqs * max_pages_per_seq < 2^31");
+      return DSA_ERR_UNSUPPORTED;
+    }
+    // the table is written here; the descriptor is shared with the read-only calls
+    a.block_table = const_cast<int32_t*>(cache->block_table);
+    a.page_size = cache->page_size;
+    a.max_pages_per_seq = cache->max_pages_per_seq;
+    a.num_pages = (int32_t)(cache->num_tokens / cache->page_size);
+  } else {
+    a.seq_start = cache->seq_start;
+  }
+  if ((st = check_ws(ws, ws_bytes, kStatusBytes)) != DSA_OK) return st;
+  a.status = reinterpret_cast<DeviceStatus*>(ws);
+  return launch_batch_plan(a, (cudaStream_t)stream);
 }
 
 dsa_status dsa_indexer_kl(const dsa_rows* rows, const float* scores, int64_t ld_scores,

@@ -1,0 +1,295 @@
+// batch_plan.cu - the block table, slot map and row map of one step from the
+// requests' lengths, with the pages popped from and pushed back on a free list
+// ("Sparse Attention in Large Language Models: Architecture Evolution and
+// Engineering Practice", section 4, item "Memory Management and KV Cache
+// Optimization": paged caches).  The rule is stated at dsa_batch_plan in
+// include/dsa.h.
+//
+// Everything follows from four prefix sums over the requests: pages handed back,
+// pages and rows asked for (the admission), and pages and rows granted.  Every
+// CTA of the one cluster computes them for itself (a few thousand requests are a
+// few microseconds of one CTA, and a second launch or a grid-wide wait would cost
+// as much), keeps the three that the rest needs in shared memory, and writes its
+// share of the rows, table entries and pages: a binary search in shared memory
+// gives a row's request.  Lengths and the free count, which may be updated in
+// place, are written by one CTA after the cluster barrier, when every CTA has
+// read them; free-list entries read (below the old count) and written (at or
+// above it) never meet, nor do table entries read (pages held) and written.
+#include <climits>
+
+#include "dsa_kernels.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kMaxSeqs = 16384;        // three int32 prefix arrays in shared memory
+constexpr int kMaxCluster = 8;
+
+// One request as the rule sees it.
+struct Request {
+  int64_t len, add;       // tokens cached, tokens asked for
+  int32_t held, need;     // pages held, pages asked for (0 when it cannot run)
+  int32_t give;           // pages handed back
+  int err;                // 0, DSA_ERR_INVALID_ARG or DSA_ERR_OUT_OF_RANGE
+  bool rel;
+  // tokens of the request's candidate rows (0 when it cannot run)
+  __device__ int64_t rows() const { return err == 0 && !rel ? add : 0; }
+};
+
+// ceil(tokens / page) for 0 <= tokens < 2^31 (32-bit: a 64-bit division costs ~5x)
+__device__ __forceinline__ int32_t pages_of(int64_t tokens, int32_t page) {
+  return (int32_t)(((uint32_t)tokens + (uint32_t)page - 1u) / (uint32_t)page);
+}
+
+__device__ __forceinline__ Request load_request(const PlanArgs& a, int b) {
+  Request r;
+  r.len = a.p.seq_len[b];
+  r.add = a.p.n_new[b];
+  r.rel = a.p.release != nullptr && a.p.release[b] != 0;
+  r.held = r.need = r.give = 0;
+  r.err = 0;
+  const int64_t width = a.block_table ? (int64_t)a.max_pages_per_seq * a.page_size
+                                      : a.num_tokens - (a.seq_start ? a.seq_start[b] : 0);
+  if (r.len < 0 || r.add < 0 || (r.rel && r.add != 0) || (a.block_table && r.len > width)) {
+    r.err = DSA_ERR_INVALID_ARG;
+  } else if (!r.rel && r.add > 0 &&
+             (r.len + r.add > width || r.len + r.add > INT_MAX || (!a.block_table && a.seq_start && a.seq_start[b] < 0))) {
+    r.err = DSA_ERR_OUT_OF_RANGE;
+  }
+  if (r.err != DSA_ERR_INVALID_ARG && a.block_table) {
+    r.held = pages_of(r.len, a.page_size);
+    if (r.rel) r.give = r.held;
+    else if (r.err == 0) r.need = pages_of(r.len + r.add, a.page_size) - r.held;
+  }
+  return r;
+}
+
+// Exclusive prefix of (x, y) over the block's threads; totals in tx, ty.
+__device__ __forceinline__ void block_scan2(int64_t& x, int64_t& y, int64_t& tx, int64_t& ty,
+                                            int64_t (*part)[kThreads / 32]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t x0 = x, y0 = y;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) { x += u; y += v; }
+  }
+  if (lane == 31) { part[0][warp] = x; part[1][warp] = y; }
+  __syncthreads();
+  if (warp == 0) {
+    int64_t u = part[0][lane], v = part[1][lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t p = __shfl_up_sync(0xffffffffu, u, o), q = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) { u += p; v += q; }
+    }
+    part[0][lane] = u;
+    part[1][lane] = v;
+  }
+  __syncthreads();
+  x += (warp ? part[0][warp - 1] : 0) - x0;
+  y += (warp ? part[1][warp - 1] : 0) - y0;
+  tx = part[0][31];
+  ty = part[1][31];
+  __syncthreads();
+}
+
+// Largest b of [0, n) with start[b] <= i, for start[0] = 0 <= i < start[n]: the
+// owner of item i (empty requests share their successor's start).
+__device__ __forceinline__ int owner(const int32_t* start, int n, int32_t i) {
+  int lo = 0, hi = n;                       // start[lo] <= i < start[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= i) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) batch_plan_kernel(const PlanArgs a) {
+  extern __shared__ int32_t sm[];
+  __shared__ int64_t part[2][kThreads / 32];
+  __shared__ int s_err, s_refused;
+  const int B = a.num_seqs, tid = threadIdx.x;
+  int32_t* tok_start = sm;                  // rows granted before request b, [B + 1]
+  int32_t* pg_start = sm + (B + 1);         // pages granted
+  int32_t* give_start = sm + 2 * (B + 1);   // pages handed back
+  const uint32_t rank = cluster_ctarank(), nranks = cluster_nctarank();
+  pdl_launch_dependents();
+  trace_kernel(a.status, DSA_KERNEL_BATCH_PLAN);
+  if (tid == 0) { s_err = INT_MAX; s_refused = 0; }
+
+  int64_t F = 0;
+  bool bad_count = false;
+  if (a.block_table) {
+    F = *a.p.free_count;
+    bad_count = F < 0 || F > a.p.free_capacity;
+    if (bad_count) F = 0;
+  }
+  __syncthreads();
+
+  cluster_arrive();                         // s_err is initialised (waited for below)
+
+  // thread i owns the requests [i * per, i * per + per)
+  const int per = (B + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
+  // pages handed back
+  int64_t give = 0, zero = 0, gives = 0, unused = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Request r = load_request(a, b);
+    give += r.give;
+    if (r.err) atomicMin(&s_err, b * 8 + r.err);
+  }
+  block_scan2(give, zero, gives, unused, part);
+  for (int b = b0; b < b1; ++b) {
+    give_start[b] = (int32_t)give;
+    give += load_request(a, b).give;
+  }
+  const int64_t have = F + gives;
+  // the admission: inclusive sums of pages and rows over every request that could run
+  int64_t need = 0, rows = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Request r = load_request(a, b);
+    need += r.need;
+    rows += r.rows();
+  }
+  int64_t ignore0, ignore1;
+  block_scan2(need, rows, ignore0, ignore1, part);
+  int64_t my_rows = 0, my_pages = 0;
+  int refused = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Request r = load_request(a, b);
+    need += r.need;
+    rows += r.rows();
+    const bool go = r.err == 0 && !r.rel && (r.need == 0 || need <= have) &&
+                    (r.add == 0 || rows <= a.p.max_tokens);
+    // granted rows and pages of b, kept in place of their sums for now
+    tok_start[b] = go ? (int32_t)r.add : 0;
+    pg_start[b] = go ? r.need : 0;
+    my_rows += tok_start[b];
+    my_pages += pg_start[b];
+    refused += !go && (r.err == DSA_ERR_INVALID_ARG || (!r.rel && r.add > 0));
+  }
+  if (refused) atomicAdd(&s_refused, refused);
+  int64_t total, taken;
+  block_scan2(my_rows, my_pages, total, taken, part);
+  for (int b = b0; b < b1; ++b) {
+    const int32_t n = tok_start[b], p = pg_start[b];
+    tok_start[b] = (int32_t)my_rows;
+    pg_start[b] = (int32_t)my_pages;
+    my_rows += n;
+    my_pages += p;
+  }
+  if (tid == 0) {
+    tok_start[B] = (int32_t)total;
+    pg_start[B] = (int32_t)taken;
+    give_start[B] = (int32_t)gives;
+  }
+  __syncthreads();
+
+  // The stack of free pages: the list, then the pages handed back.
+  const int64_t W = a.max_pages_per_seq;
+  const auto handed_back = [&](int32_t i) {
+    const int b = owner(give_start, B, i);
+    return a.block_table[(int64_t)b * W + (i - give_start[b])];
+  };
+  // The k-th page taken, -1 when its id lies outside the cache.
+  const auto taken_page = [&](int32_t k) {
+    const int64_t i = have - 1 - k;
+    const int32_t pg = i < F ? a.p.free_pages[i] : handed_back((int32_t)(i - F));
+    return pg >= 0 && pg < a.num_pages ? pg : -1;
+  };
+  const int gid = (int)rank * kThreads + tid, step = (int)nranks * kThreads;
+  const int32_t n_rows = (int32_t)total;
+  const int last = n_rows > 0 ? owner(tok_start, B, n_rows - 1) : 0;
+  for (int64_t t64 = gid; t64 < a.p.max_tokens; t64 += step) {
+    const int32_t t = (int32_t)t64;
+    int b = last;
+    int32_t pos = -1;
+    int64_t slot = -1;
+    if (t < n_rows) {
+      b = owner(tok_start, B, t);
+      const int32_t len = a.p.seq_len[b];
+      pos = len + (t - tok_start[b]);
+      if (a.block_table) {
+        const int32_t pg = pos / a.page_size, held = pages_of(len, a.page_size);
+        int32_t page = pg >= held ? taken_page(pg_start[b] + pg - held) : a.block_table[(int64_t)b * W + pg];
+        if (page < 0 || page >= a.num_pages) {
+          atomicMin(&s_err, b * 8 + DSA_ERR_OUT_OF_RANGE);
+          page = -1;
+        }
+        if (page >= 0) slot = (int64_t)page * a.page_size + (pos - pg * a.page_size);
+      } else {
+        slot = (int64_t)(a.seq_start ? a.seq_start[b] : 0) + pos;
+      }
+    }
+    a.p.row_seq[t] = b;
+    a.p.row_klen[t] = pos + 1;
+    a.p.tok_pos[t] = pos;
+    a.p.slot[t] = slot;
+  }
+  for (int k = gid; k < (int)taken; k += step) {
+    const int b = owner(pg_start, B, k);
+    const int32_t held = pages_of(a.p.seq_len[b], a.page_size);
+    a.block_table[(int64_t)b * W + held + (k - pg_start[b])] = taken_page(k);
+  }
+  const int64_t left = min(have - taken, (int64_t)a.p.free_capacity);
+  for (int64_t i = F + gid; i < left; i += step) a.p.free_pages[i] = handed_back((int32_t)(i - F));
+  for (int b = gid; b <= B; b += step) a.p.tok_start[b] = tok_start[b];
+
+  // the lowest request in error, over the cluster
+  cluster_wait();
+  __syncthreads();
+  if (rank != 0 && tid == 0 && s_err != INT_MAX)
+    asm volatile("red.relaxed.cluster.shared::cluster.min.s32 [%0], %1;" ::"r"(mapa(&s_err, 0)), "r"(s_err)
+                 : "memory");
+  cluster_sync();                           // every CTA has read the lengths and the free count
+  if (rank != 0) return;
+  if (tid == 0 && s_err != INT_MAX) set_status(a.status, s_err & 7, s_err >> 3);
+  for (int b = tid; b < B; b += kThreads) {
+    const Request r = load_request(a, b);
+    const int32_t n = tok_start[b + 1] - tok_start[b];
+    a.p.seq_len_out[b] = r.rel && r.err == 0 ? 0 : (int32_t)(r.len + n);
+  }
+  if (tid == 0) {
+    if (bad_count || have - taken > left) set_status(a.status, DSA_ERR_INVALID_ARG, -1);
+    if (a.block_table) *a.p.free_count_out = (int32_t)left;
+    a.p.totals[0] = n_rows;
+    a.p.totals[1] = (int32_t)taken;
+    a.p.totals[2] = s_refused;
+    a.p.totals[3] = (int32_t)gives;
+  }
+}
+
+}  // namespace
+
+int batch_plan_max_seqs() { return kMaxSeqs; }
+
+dsa_status launch_batch_plan(const PlanArgs& a, cudaStream_t stream) {
+  const size_t smem_max = (size_t)3 * (kMaxSeqs + 1) * sizeof(int32_t);
+  static std::atomic<bool> attr[kMaxDevices] = {};
+  if (dsa_status st = set_smem_limit_once(reinterpret_cast<const void*>(batch_plan_kernel), smem_max, attr))
+    return st;
+  int ctas = 1;
+  while (ctas < kMaxCluster && (int64_t)ctas * kThreads < a.p.max_tokens) ctas <<= 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)3 * (a.num_seqs + 1) * sizeof(int32_t);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)ctas;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, batch_plan_kernel, a);
+  if (e != cudaSuccess) {
+    set_error("batch plan launch failed: %s", cudaGetErrorString(e));
+    return DSA_ERR_CUDA;
+  }
+  return DSA_OK;
+}
+
+}  // namespace dsa

@@ -420,6 +420,8 @@ struct CacheMap {
   int32_t max_pages_per_seq;
   int32_t num_pages;
   int64_t num_tokens;
+  // Whether a row depends on the sequence (else every sequence is the cache from row 0 on).
+  __device__ __forceinline__ bool uses_seq() const { return block_table != nullptr || seq_start != nullptr; }
   __device__ __forceinline__ int64_t row(int b, int s, DeviceStatus* st, bool* ok) const {
     if (block_table != nullptr) {
       int pg = page_shift >= 0 ? (s >> page_shift) : s / page_size;

@@ -52,8 +52,9 @@ struct MlaArgs {
   float sm_scale;
   const void* q;              // [T, H, d_c + d_r]
   const int32_t* idx;         // [T, topk]
-  const void* latent;         // [num_tokens, d_c + d_r]
+  const void* latent;         // [num_tokens, d_c + d_r] or packed rows
   CacheMap map;
+  int num_seqs;
   void* out;                  // [T, H, d_c]
   float* lse;                 // [T, H] or null
   DeviceStatus* status;
@@ -75,13 +76,43 @@ struct AppendArgs {
   const float* k_new;         // [n_new, d_I] fp32
   const void* latent_new;     // [n_new, d_c + d_r] in the latent cache's dtype
   int d_idx;
-  int latent_row_bytes;       // (d_c + d_r) * element size, a multiple of 16
+  int latent_row_bytes;       // of the cache, a multiple of 16
+  int latent_new_row_bytes;   // of latent_new: (d_c + d_r) * element size, a multiple of 16
   dsa_dtype idx_dtype;
   void* idx_k;                // written: [num_tokens, d_I] e4m3 | f32
   float* idx_k_scale;         // written: [num_tokens] (e4m3 only)
-  void* latent;               // written: [num_tokens, d_c + d_r]
+  void* latent;               // written: [num_tokens, d_c + d_r] or packed rows
   CacheMap map;
   int num_seqs;
+  DeviceStatus* status;
+  const int64_t* slot;        // [n_new] physical rows (tok_seq / tok_pos unused), or null
+  bool int4;                  // packed latent rows: latent_new is bf16
+  int d_c, d_r;
+};
+
+struct ReadArgs {
+  int n;
+  const int64_t* slot;        // [n]
+  const void* idx_k;
+  const float* idx_k_scale;
+  const void* latent;
+  float* k_out;               // [n, d_I] or null
+  void* latent_out;           // [n, d_c + d_r] or null
+  int d_idx, d_c, d_r;
+  int latent_row_bytes;       // of the cache
+  dsa_dtype idx_dtype;
+  bool int4;
+  int64_t num_tokens;
+  DeviceStatus* status;
+};
+
+struct PlanArgs {
+  dsa_plan p;
+  int num_seqs;
+  int32_t* block_table;       // written; null: contiguous
+  const int32_t* seq_start;
+  int32_t page_size, max_pages_per_seq, num_pages;
+  int64_t num_tokens;
   DeviceStatus* status;
 };
 
@@ -120,6 +151,9 @@ size_t mla_ws_bytes(int num_rows, int n_heads, int d_c, int splits);
 
 dsa_status launch_cache_append(const AppendArgs& a, cudaStream_t stream);
 int cache_append_max_d_idx();
+dsa_status launch_cache_read(const ReadArgs& a, cudaStream_t stream);
+dsa_status launch_batch_plan(const PlanArgs& a, cudaStream_t stream);
+int batch_plan_max_seqs();
 
 // Indexer warm-up: KL(p || softmax(I)) per row, its gradient g, and the
 // backward of the indexer scores to q_I, w and k_I.

@@ -13,6 +13,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include "dsa_int4.cuh"
 #include "dsa_kernels.cuh"
 
 namespace dsa {
@@ -64,8 +65,8 @@ __global__ void __launch_bounds__(128) indexer_simt_kernel(IndexerArgs a) {
 }
 
 // grid (T, H/8), block 128.  Each block: one row, 8 heads.
-// smem: q [8][D] + kv [16][D] + z [8][16] floats.
-template <typename T>
+// smem: q [8][D] + kv [16][D] + z [8][16] floats.  kInt4: packed latent rows.
+template <typename T, bool kInt4>
 __global__ void __launch_bounds__(128) mla_simt_kernel(MlaArgs a) {
   constexpr int HB = 8, KC = 16;
   extern __shared__ float sm[];
@@ -98,8 +99,9 @@ __global__ void __launch_bounds__(128) mla_simt_kernel(MlaArgs a) {
       const int s = (c0 + threadIdx.x < a.topk) ? idx[c0 + threadIdx.x] : -1;
       int64_t pr = -1;
       if (s >= 0) {
-        bool ok = true;
-        pr = a.map.row(seq, s, a.status, &ok);
+        bool ok = (seq >= 0 && seq < a.num_seqs) || !a.map.uses_seq();
+        if (ok) pr = a.map.row(seq, s, a.status, &ok);
+        else set_status(a.status, DSA_ERR_OUT_OF_RANGE, t);
         if (!ok) pr = -1;
       }
       prow[threadIdx.x] = pr;
@@ -108,7 +110,15 @@ __global__ void __launch_bounds__(128) mla_simt_kernel(MlaArgs a) {
     const T* lat = static_cast<const T*>(a.latent);
     for (int i = threadIdx.x; i < KC * D; i += blockDim.x) {
       int j = i / D, d = i - j * D;
-      kv[i] = prow[j] >= 0 ? load_elem(lat, prow[j] * D + d) : 0.f;
+      if constexpr (kInt4) {
+        const Int4Row ly = int4_row(a.d_c, a.d_r);
+        const uint8_t* row = static_cast<const uint8_t*>(a.latent) + prow[j] * ly.bytes;
+        kv[i] = prow[j] < 0 ? 0.f
+                : d < DC    ? int4_dim(row, d, ly)
+                            : load_elem(reinterpret_cast<const __nv_bfloat16*>(row + ly.rope), d - DC);
+      } else {
+        kv[i] = prow[j] >= 0 ? load_elem(lat, prow[j] * D + d) : 0.f;
+      }
     }
     __syncthreads();
     // logits: thread -> (head, key) pair, 8 x 16 = 128
@@ -178,23 +188,22 @@ dsa_status launch_indexer_simt(const IndexerArgs& a, cudaStream_t stream) {
 
 dsa_status launch_mla_simt(const MlaArgs& a, cudaStream_t stream) {
   if (a.num_rows == 0) return DSA_OK;
-  if (a.n_heads % 8 != 0 || a.d_c % 16 != 0 || a.d_c > 512) return DSA_ERR_UNSUPPORTED;
+  if (a.n_heads % 8 != 0 || a.d_c % 16 != 0 || a.d_c > 512) {
+    set_error("the CUDA-core attention takes H %% 8 == 0, d_c %% 16 == 0 and d_c <= 512");
+    return DSA_ERR_UNSUPPORTED;
+  }
   const int D = a.d_c + a.d_r;
   size_t smem = (size_t)(8 * D + 16 * D + 8 * 16) * sizeof(float);
   dim3 grid(a.num_rows, a.n_heads / 8);
-  cudaError_t e;
-  if (a.mla_dtype == DSA_BF16) {
-    e = cudaFuncSetAttribute(mla_simt_kernel<__nv_bfloat16>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return DSA_ERR_CUDA;
-    mla_simt_kernel<__nv_bfloat16><<<grid, 128, smem, stream>>>(a);
-  } else {
-    e = cudaFuncSetAttribute(mla_simt_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem);
-    if (e != cudaSuccess) return DSA_ERR_CUDA;
-    mla_simt_kernel<float><<<grid, 128, smem, stream>>>(a);
-  }
-  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  const auto run = [&](void (*kernel)(MlaArgs)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+      return DSA_ERR_CUDA;
+    kernel<<<grid, 128, smem, stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  };
+  if (a.mla_dtype == DSA_INT4) return run(mla_simt_kernel<__nv_bfloat16, true>);
+  if (a.mla_dtype == DSA_BF16) return run(mla_simt_kernel<__nv_bfloat16, false>);
+  return run(mla_simt_kernel<float, false>);
 }
 
 }  // namespace dsa

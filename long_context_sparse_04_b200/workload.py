@@ -32,11 +32,28 @@ def q_group_for(cfg) -> int:
     return cfg.rows_per_seq if cfg.rows_per_seq in (1, 2, 4) else 1
 
 
+def pack_latents(dims, latent):
+    """Packed 4-bit rows (uint8 [n, row bytes]) of bf16 latent rows on a device."""
+    import torch
+    n = latent.shape[0]
+    packed = torch.empty((n, N.dsa_latent_row_bytes(dims)), dtype=torch.uint8, device=latent.device)
+    slot = torch.arange(n, dtype=torch.int64, device=latent.device)
+    ws = torch.zeros(N.dsa_workspace_size(dims, None, N.DSA_OP_CACHE_APPEND), dtype=torch.uint8, device=latent.device)
+    cache = N.dsa_cache(latent=_vp(packed), num_seqs=1, num_tokens=n)
+    stream = ctypes.c_void_p(torch.cuda.current_stream(latent.device).cuda_stream)
+    with torch.cuda.device(latent.device):
+        N.dsa_cache_append_slots(dims, cache, n, _vp(slot), None, _vp(latent), _vp(ws), ws.numel(), stream)
+        st = N.dsa_read_device_status(_vp(ws), stream)
+    assert st == (0, -1), f"latent row {st[1]} has an infinity or NaN"
+    return packed
+
+
 class DeviceWorkload:
     """One workload resident on a CUDA device, with the C-ABI descriptors."""
 
     def __init__(self, inp: dict, device="cuda", algo: int = N.DSA_ALGO_AUTO,
-                 q_group: int | None = None):
+                 q_group: int | None = None, int4: bool = False):
+        """int4: keep the latent cache in packed 4-bit rows (bf16 workloads)."""
         import torch
         self.torch = torch
         self.inp = inp
@@ -68,8 +85,11 @@ class DeviceWorkload:
             n_idx_heads=int(inp["h_idx"]), d_idx=int(inp["d_idx"]), n_heads=self.H,
             d_c=self.d_c, d_r=int(inp["d_r"]), topk=self.topk,
             idx_dtype=N.DSA_FP8_E4M3 if inp["idx_dtype"] == "e4m3" else N.DSA_F32,
-            mla_dtype=N.DSA_BF16 if self.mla_bf16 else N.DSA_F32,
+            mla_dtype=N.DSA_INT4 if int4 else N.DSA_BF16 if self.mla_bf16 else N.DSA_F32,
             sm_scale=float(inp["sm_scale"]), algo=algo)
+        if int4:
+            assert self.mla_bf16, "packed latent rows are made of bf16 rows"
+            self.latent = pack_latents(self.dims, self.latent)
         self.rows = N.dsa_rows(num_rows=T, row_seq=_vp(self.row_seq), row_klen=_vp(self.row_klen),
                                max_klen=self.max_klen,
                                q_group=q_group if q_group is not None else q_group_for(cfg))
@@ -184,3 +204,102 @@ class DeviceWorkload:
             else lat.cpu().numpy()
         ks = None if self.k_scale is None else self.k_scale.cpu().numpy()
         return self.k_idx.cpu().numpy(), ks, lat
+
+
+class DevicePlanner:
+    """The paging state of a batch of request slots, planned on the GPU: lengths,
+    block table and free list live in device memory and each plan() (one
+    dsa_batch_plan, in place) advances them by ``n_new`` and ``release``."""
+
+    def __init__(self, num_seqs: int, page_size: int, num_pages: int, max_pages_per_seq: int, max_tokens: int,
+                 device="cuda"):
+        import torch
+        self.torch = torch
+        dev = self.device = torch.device(device)
+        self.num_seqs, self.max_tokens, self.max_len = num_seqs, max_tokens, max_pages_per_seq * page_size
+        zeros = lambda *shape, dtype=torch.int32: torch.zeros(shape, dtype=dtype, device=dev)  # noqa: E731
+        self.seq_len, self.n_new, self.release = zeros(num_seqs), zeros(num_seqs), zeros(num_seqs)
+        self.block_table = torch.full((num_seqs, max_pages_per_seq), -1, dtype=torch.int32, device=dev)
+        self.free_pages = torch.arange(num_pages, dtype=torch.int32, device=dev)
+        self.free_count = torch.full((1,), num_pages, dtype=torch.int32, device=dev)
+        self.tok_start, self.totals = zeros(num_seqs + 1), zeros(4)
+        self.row_seq, self.row_klen, self.tok_pos = zeros(max_tokens), zeros(max_tokens), zeros(max_tokens)
+        self.slot = zeros(max_tokens, dtype=torch.int64)
+        self.cache = N.dsa_cache(block_table=_vp(self.block_table), page_size=page_size,
+                                 max_pages_per_seq=max_pages_per_seq, num_seqs=num_seqs,
+                                 num_tokens=num_pages * page_size)
+        self._plan = N.dsa_plan(
+            seq_len=_vp(self.seq_len), n_new=_vp(self.n_new), release=_vp(self.release),
+            seq_len_out=_vp(self.seq_len), free_count=_vp(self.free_count), free_count_out=_vp(self.free_count),
+            free_pages=_vp(self.free_pages), free_capacity=num_pages, max_tokens=max_tokens,
+            tok_start=_vp(self.tok_start), row_seq=_vp(self.row_seq), row_klen=_vp(self.row_klen),
+            tok_pos=_vp(self.tok_pos), slot=_vp(self.slot), totals=_vp(self.totals))
+        self._ws = zeros(N.dsa_workspace_size(None, None, N.DSA_OP_BATCH_PLAN), dtype=torch.uint8)
+
+    @property
+    def stream(self):
+        return ctypes.c_void_p(self.torch.cuda.current_stream(self.device).cuda_stream)
+
+    def plan(self):
+        N.dsa_batch_plan(self.cache, self._plan, _vp(self._ws), self._ws.numel(), self.stream)
+
+    def status(self):
+        return N.dsa_read_device_status(_vp(self._ws), self.stream)
+
+    def rows(self, q_group: int = 1):
+        """dsa_rows of the whole (padded) batch."""
+        return N.dsa_rows(num_rows=self.max_tokens, row_seq=_vp(self.row_seq), row_klen=_vp(self.row_klen),
+                          max_klen=self.max_len, q_group=q_group)
+
+
+class PagedCache:
+    """The caches of one layer behind a DevicePlanner: FP8 indexer keys, and the
+    latents in bf16 or in packed 4-bit rows."""
+
+    def __init__(self, planner: DevicePlanner, n_heads: int = 128, topk: int = 2048, int4: bool = True,
+                 sm_scale: float | None = None, q_group: int = 1):
+        torch = self.torch = planner.torch
+        self.planner = planner
+        d_c, d_r, d_idx = 512, 64, 128
+        self.sm_scale = (d_c + d_r) ** -0.5 if sm_scale is None else sm_scale
+        self.dims = N.dsa_dims(n_idx_heads=64, d_idx=d_idx, n_heads=n_heads, d_c=d_c, d_r=d_r, topk=topk,
+                               idx_dtype=N.DSA_FP8_E4M3, mla_dtype=N.DSA_INT4 if int4 else N.DSA_BF16,
+                               sm_scale=self.sm_scale, algo=N.DSA_ALGO_AUTO)
+        p, dev = planner, planner.device
+        n = int(p.cache.num_tokens)
+        self.latent = torch.zeros((n, N.dsa_latent_row_bytes(self.dims)), dtype=torch.uint8, device=dev)
+        self.idx_k = torch.zeros((n, d_idx), dtype=torch.uint8, device=dev)
+        self.idx_k_scale = torch.ones(n, dtype=torch.float32, device=dev)
+        self.cache = N.dsa_cache(latent=_vp(self.latent), idx_k=_vp(self.idx_k), idx_k_scale=_vp(self.idx_k_scale),
+                                 block_table=p.cache.block_table, page_size=p.cache.page_size,
+                                 max_pages_per_seq=p.cache.max_pages_per_seq, num_seqs=p.num_seqs, num_tokens=n)
+        self.rows = p.rows(q_group)
+        self.idx = torch.full((p.max_tokens, topk), -1, dtype=torch.int32, device=dev)
+        nb = N.dsa_workspace_size(self.dims, self.rows, N.DSA_OP_DECODE_STEP)
+        self._ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+        N.dsa_workspace_init(_vp(self._ws), nb, p.stream)
+
+    def _args(self):
+        return _vp(self._ws), self._ws.numel(), self.planner.stream
+
+    def append(self, k_new, latent_new):
+        """The planned step's tokens (rows of max_tokens) into the caches."""
+        N.dsa_cache_append_slots(self.dims, self.cache, self.planner.max_tokens, _vp(self.planner.slot), _vp(k_new),
+                                 _vp(latent_new), *self._args())
+
+    def read(self, slot, k_out=None, latent_out=None):
+        """Cached tokens by physical row, as the values they stand for."""
+        N.dsa_cache_read(self.dims, self.cache, int(slot.shape[0]), _vp(slot), _vp(k_out), _vp(latent_out), *self._args())
+
+    def decode_step(self, q_idx, q_scale, w, q, out, lse=None):
+        """The three stages over the planned rows; rows behind the last give 0 and -inf."""
+        N.dsa_decode_step(self.dims, self.rows, self.cache, _vp(q_idx), _vp(q_scale), _vp(w), _vp(q), _vp(out), _vp(lse),
+                          None, _vp(self.idx), *self._args())
+        return out, lse
+
+    def indices(self):
+        """The last step's selection [max_tokens, topk]."""
+        return self.idx
+
+    def status(self):
+        return N.dsa_read_device_status(*self._args()[::2])

@@ -486,3 +486,168 @@ def indexer_backward_row(q: np.ndarray, w: np.ndarray, k: np.ndarray, g: np.ndar
     dq = gd.T @ k                             # [H_I, d_I]
     dk = gd @ q                               # [n, d_I]
     return dq, dw, dk
+
+
+# ----------------------------------------------------------------------------
+# Packed latent rows: 4-bit codes with one 8-bit scale per 16 latent dims
+# ----------------------------------------------------------------------------
+#
+# "Sparse Attention in Large Language Models: Architecture Evolution and
+# Engineering Practice", section 4, item "Memory Management and KV Cache
+# Optimization": the latent cache is what bounds the batch.  The pages give no
+# 4-bit format; the one taken here is stated in include/dsa.h.
+
+INT4_GROUP = 16
+INT4_SCALE_MAX = 0xF7
+
+
+def int4_scale_decode(codes: np.ndarray) -> np.ndarray:
+    """Value of scale bytes: 5 exponent bits (bias 15), 3 mantissa bits,
+    subnormals (exponent field 0) in steps of 2^-17."""
+    c = np.asarray(codes, dtype=np.int64)
+    e, m = c >> 3, c & 7
+    return np.where(e > 0, np.ldexp(1.0 + m / 8.0, e - 15), m * 2.0 ** -17)
+
+
+def int4_scale_encode(r: np.ndarray) -> np.ndarray:
+    """Nearest scale byte to each r >= 0, ties to the even byte, at most 0xF7."""
+    r = np.asarray(r, dtype=np.float64)
+    grid = int4_scale_decode(np.arange(INT4_SCALE_MAX + 1))
+    hi = np.clip(np.searchsorted(grid, r), 1, INT4_SCALE_MAX)
+    lo = hi - 1
+    d_hi, d_lo = grid[hi] - r, r - grid[lo]
+    return np.where((d_hi < d_lo) | ((d_hi == d_lo) & (hi % 2 == 0)), hi, lo).astype(np.uint8)
+
+
+def int4_row_bytes(d_c: int, d_r: int) -> int:
+    return -(-(d_c // 2 + 2 * d_r + d_c // INT4_GROUP) // 16) * 16
+
+
+def int4_quantise(c: np.ndarray):
+    """Codes (int, [n, d_c]) and scale bytes ([n, d_c/16]) of latent dims c
+    (float32, finite): both divisions in fp32, both roundings to nearest even."""
+    c = np.asarray(c, dtype=np.float32)
+    if not np.all(np.isfinite(c)):
+        raise ValueError("int4_quantise: non-finite latent")
+    n, d_c = c.shape
+    g = c.reshape(n, d_c // INT4_GROUP, INT4_GROUP)
+    scale = int4_scale_encode(np.max(np.abs(g), axis=2) / np.float32(7))
+    s = int4_scale_decode(scale).astype(np.float32)[:, :, None]
+    y = np.divide(g, s, out=np.zeros_like(g), where=s > 0).astype(np.float64)
+    return np.clip(np.rint(y), -7, 7).astype(np.int64).reshape(n, d_c), scale
+
+
+def int4_pack(latent_bits: np.ndarray, d_c: int, d_r: int) -> np.ndarray:
+    """Packed rows (uint8 [n, int4_row_bytes]) of bf16 rows (bit patterns uint16)."""
+    q, scale = int4_quantise(bf16_decode(latent_bits[:, :d_c]).astype(np.float32))
+    n = q.shape[0]
+    rows = np.zeros((n, int4_row_bytes(d_c, d_r)), np.uint8)
+    words = np.zeros((n, d_c // 8), np.uint64)
+    for d in range(8):
+        shift = np.uint64(4 * (d // 2) + (16 if d % 2 else 0))
+        words |= (q[:, d::8] & 15).astype(np.uint64) << shift
+    rows[:, : d_c // 2] = words.astype("<u4").view(np.uint8)
+    rope = d_c // 2
+    rows[:, rope: rope + 2 * d_r] = np.ascontiguousarray(latent_bits[:, d_c:]).astype("<u2").view(np.uint8)
+    rows[:, rope + 2 * d_r: rope + 2 * d_r + d_c // INT4_GROUP] = scale
+    return rows
+
+
+def int4_unpack(rows: np.ndarray, d_c: int, d_r: int) -> np.ndarray:
+    """The values of packed rows, float64 [n, d_c + d_r]."""
+    rows = np.asarray(rows, dtype=np.uint8)
+    n = rows.shape[0]
+    words = np.ascontiguousarray(rows[:, : d_c // 2]).view("<u4")
+    out = np.empty((n, d_c + d_r))
+    for d in range(8):
+        v = (words >> np.uint32(4 * (d // 2) + (16 if d % 2 else 0))) & np.uint32(15)
+        out[:, d:d_c:8] = np.where(v >= 8, v.astype(np.int64) - 16, v.astype(np.int64))
+    rope = d_c // 2
+    s = int4_scale_decode(rows[:, rope + 2 * d_r: rope + 2 * d_r + d_c // INT4_GROUP])
+    out[:, :d_c] *= np.repeat(s, INT4_GROUP, axis=1)
+    out[:, d_c:] = bf16_decode(np.ascontiguousarray(rows[:, rope: rope + 2 * d_r]).view("<u2"))
+    return out
+
+
+# ----------------------------------------------------------------------------
+# Batch plan: one request after the other, with Python lists as the state
+# ----------------------------------------------------------------------------
+
+def batch_plan(seq_len, n_new, release, free_list, block_table, page_size, num_pages, max_tokens,
+               seq_start=None, num_tokens=0):
+    """The rule of dsa_batch_plan, request by request.
+
+    free_list: the page ids in use of the free list, bottom first (paged);
+    block_table: [B, W] or None (contiguous: seq_start [B] or None).
+    Returns a dict: seq_len, free_list, block_table, rows (a list of
+    (request, position, slot)), start [B + 1], totals [4], error (status, detail).
+    """
+    B, P = len(seq_len), page_size
+    table = None if block_table is None else np.array(block_table, copy=True)
+    W = 0 if table is None else table.shape[1]
+    free = list(free_list) if table is not None else []
+    lens, errors, runs, handed = [int(x) for x in seq_len], {}, [], 0
+    up = lambda n: -(-n // P)  # noqa: E731
+    old = list(lens)
+    for b in range(B):
+        rel = release is not None and int(release[b]) != 0
+        n, L = int(n_new[b]), old[b]
+        if L < 0 or n < 0 or (rel and n != 0) or (table is not None and L > W * P):
+            errors[b] = "invalid"
+            continue
+        if rel:
+            if table is not None:
+                free += [int(x) for x in table[b, : up(L)]]
+                handed += up(L)
+            lens[b] = 0
+            continue
+        if n == 0:
+            runs.append((b, 0))
+            continue
+        if table is not None:
+            too_long = L + n > W * P
+        else:
+            start = 0 if seq_start is None else int(seq_start[b])
+            too_long = start < 0 or start + L + n > num_tokens
+        if too_long or L + n > 2 ** 31 - 1:
+            errors[b] = "range"
+        else:
+            runs.append((b, n))
+    have, asked_pages, asked_rows, taken = len(free), 0, 0, 0
+    rows, granted = [], {}
+    for b, n in runs:
+        L = old[b]
+        need = up(L + n) - up(L) if table is not None else 0
+        asked_pages += need
+        asked_rows += n
+        if (need and asked_pages > have) or (n and asked_rows > max_tokens):
+            continue
+        granted[b] = n
+        for j in range(need):
+            page = free.pop()
+            taken += 1
+            if not 0 <= page < num_pages:
+                errors.setdefault(b, "range")
+                page = -1
+            table[b, up(L) + j] = page
+        for j in range(n):
+            pos = L + j
+            if table is not None:
+                page = int(table[b, pos // P])
+                ok = 0 <= page < num_pages
+                if not ok:
+                    errors.setdefault(b, "range")
+                slot = page * P + pos % P if ok else -1
+            else:
+                slot = (0 if seq_start is None else int(seq_start[b])) + pos
+            rows.append((b, pos, slot))
+        lens[b] = L + n
+    start = [0]
+    for b in range(B):
+        start.append(start[-1] + granted.get(b, 0))
+    refused = sum(1 for b in range(B) if errors.get(b) == "invalid" or
+                  (b not in granted and int(n_new[b]) > 0 and errors.get(b) != "invalid"))
+    first = min(errors) if errors else None
+    return dict(seq_len=lens, free_list=free, block_table=table, rows=rows, start=start,
+                totals=[len(rows), taken, refused, handed],
+                error=("ok", -1) if first is None else (errors[first], first))

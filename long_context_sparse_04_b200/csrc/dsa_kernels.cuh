@@ -143,6 +143,8 @@ size_t topk_ws_bytes();
 dsa_status launch_mla_simt(const MlaArgs& a, cudaStream_t stream);
 dsa_status launch_mla_tc(const MlaArgs& a, cudaStream_t stream);
 bool mla_tc_supported(const MlaArgs& a);
+dsa_status launch_mla_int4_tc(const MlaArgs& a, cudaStream_t stream);
+bool mla_int4_tc_supported(const MlaArgs& a);
 int mla_tc_splits(int num_rows);
 // Whether a top-k of `num_rows` rows of at most `max_klen` keys runs as
 // clusters (else one CTA per row, streaming).

@@ -1,0 +1,55 @@
+// mla_common.cuh - what the tensor-core attention kernels (bf16 rows, packed
+// 4-bit rows) share: softmax constants, roundings, and the arrival tickets of the
+// key splits.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "dsa_common.cuh"
+
+namespace dsa {
+
+constexpr int kMaxSplits = 8;                 // key splits of a decode row, a power of 2
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescale = 8.0f;
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// 2^x with the hardware approximation (ex2.approx.ftz.f32; 2^-inf = +0).
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// f[0..8) * inv as eight bf16 (round to nearest even) in one 16-byte piece.
+__device__ __forceinline__ uint4 pack8(const float* f, float inv) {
+  return make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
+                    pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
+}
+// Arrival ticket of one of a row's key splits: the slot holds (launch id << 32 |
+// arrivals); a slot tagged with another launch (an earlier one, or never
+// written) counts as empty, and the last arrival resets the count, so the
+// slots need no clearing between launches.
+// Returns the arrivals of this launch, this one included (0 if the CAS loop,
+// which only ever competes with the row's other splits, were to run away).
+__device__ __forceinline__ uint32_t take_ticket(unsigned long long* slot, uint32_t id, DeviceStatus* st) {
+  unsigned long long cur = *reinterpret_cast<volatile unsigned long long*>(slot);
+  for (int it = 0; it < 1 << 16; ++it) {
+    const unsigned long long nv =
+        (uint32_t)(cur >> 32) == id ? cur + 1ull : ((unsigned long long)id << 32) | 1ull;
+    const unsigned long long got = atomicCAS(slot, cur, nv);
+    if (got == cur) return (uint32_t)nv;
+    cur = got;
+  }
+  set_status(st, DSA_ERR_TIMEOUT, 29);
+  return 0u;
+}
+
+uint32_t next_launch_id();
+
+}  // namespace dsa

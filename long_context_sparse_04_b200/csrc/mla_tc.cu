@@ -41,9 +41,8 @@
 // the 896 threads x 72 the kernel is launched with (checked before launch).
 // TMEM: S double buffer (2 x 64 cols), P double buffer (2 x 32 cols of bf16x2),
 // O (256 cols).
-#include <cuda_bf16.h>
-
 #include "dsa_kernels.cuh"
+#include "mla_common.cuh"
 
 namespace dsa {
 namespace {
@@ -52,7 +51,6 @@ constexpr int kH = 128, kDC = 512, kDR = 64, kD = kDC + kDR;
 constexpr int kBlk = 64;
 constexpr int kNS = 3;
 constexpr int kMaxKeys = 2048;
-constexpr int kMaxSplits = 8;                 // key splits of a decode row, a power of 2
 constexpr int kGatherWarp0 = 1, kGatherWarps = 15;
 constexpr int kGatherThreads = 32 * kGatherWarps;       // 480
 constexpr int kExWarp0 = 16;                            // warps 16-19
@@ -65,9 +63,6 @@ static_assert(kThreads * kRegsLaunch <= 65536, "launch registers exceed the SM's
 static_assert(kThreads % 32 == 0 && (kMaxSplits & (kMaxSplits - 1)) == 0, "layout");
 constexpr int kPieces = 36;                 // 16-byte pieces of one key's 288 dims per CTA
 constexpr uint32_t kColS = 0, kColP = 128, kColO = 256, kTmemCols = 512;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescale = 8.0f;
 // One exchanged tile of partial logits of 128 heads x 64 keys in the transport
 // format below (row max + 16-bit fixed-point distance to it).
 struct __align__(16) XTile {
@@ -106,18 +101,6 @@ constexpr uint32_t kMergeO = 64 * 1024, kMergeMl = kH * 8, kMergeTx = kMergeO + 
 static_assert(offsetof(MlaSmem, kv) == kSendO && offsetof(MlaSmem, kv) + 2 * sizeof(MlaSmem::kv[0]) == kStage4 &&
                   offsetof(MlaSmem, kv_rope) == kSendMl && kRecvMl + kMergeMl <= kSendMl + sizeof(MlaSmem::kv_rope),
               "cluster merge layout");
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-
-// 2^x with the hardware approximation (ex2.approx.ftz.f32; 2^-inf = +0).
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // Transport format of a partial logit row (log2 domain) between the two CTAs:
 // the row max m (fp32) and, per key, u = round(1024 * (m - z)) as a 16-bit
@@ -168,11 +151,6 @@ __device__ __forceinline__ void load_o(uint32_t taddr, bool empty, float (&o)[32
   tmem_ld32(taddr, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
   tmem_wait_ld();
 }
-// f[0..8) * inv as eight bf16 (round to nearest even) in one 16-byte piece.
-__device__ __forceinline__ uint4 pack8(const float* f, float inv) {
-  return make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
-                    pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
-}
 // Row h of the CTA's finished output tile in shared memory: 256 bf16 dims as
 // 32 pieces of 16 bytes, piece c stored at c ^ (h % 32) so that a warp's 32
 // rows hit distinct banks; o * inv are dims [8 c0, 8 c0 + 32).
@@ -181,25 +159,6 @@ __device__ __forceinline__ void stage_bf16(uint8_t* stg, int h, int c0, const fl
   for (int q = 0; q < 4; ++q)
     *reinterpret_cast<uint4*>(stg + h * 512 + (((c0 + q) ^ (h & 31)) << 4)) = pack8(&o[8 * q], inv);
 }
-// Arrival ticket of one of a row's key splits: the slot holds (launch id << 32 |
-// arrivals); a slot tagged with another launch (an earlier one, or never
-// written) counts as empty, and the last arrival resets the count, so the
-// slots need no clearing between launches.
-// Returns the arrivals of this launch, this one included (0 if the CAS loop,
-// which only ever competes with the row's other splits, were to run away).
-__device__ __forceinline__ uint32_t take_ticket(unsigned long long* slot, uint32_t id, DeviceStatus* st) {
-  unsigned long long cur = *reinterpret_cast<volatile unsigned long long*>(slot);
-  for (int it = 0; it < 1 << 16; ++it) {
-    const unsigned long long nv =
-        (uint32_t)(cur >> 32) == id ? cur + 1ull : ((unsigned long long)id << 32) | 1ull;
-    const unsigned long long got = atomicCAS(slot, cur, nv);
-    if (got == cur) return (uint32_t)nv;
-    cur = got;
-  }
-  set_status(st, DSA_ERR_TIMEOUT, 29);
-  return 0u;
-}
-
 __device__ __forceinline__ void tstamp(long long* tr, uint32_t rank, int ev, int j) {
   if (tr != nullptr && blockIdx.x < 2 && j < kTraceBlocks)
     tr[((int)rank * kTraceEvents + ev) * kTraceBlocks + j] = clock64();
@@ -792,6 +751,14 @@ int mla_tc_splits(int num_rows) {
   return s;
 }
 
+// A launch id for the split arrival tickets: distinct for consecutive launches, never 0.
+uint32_t next_launch_id() {
+  static std::atomic<uint32_t> launch_seq{0};
+  uint32_t id;
+  do id = launch_seq.fetch_add(1u) + 1u; while (id == 0u);
+  return id;
+}
+
 // Split-K scratch: partial O (fp32) and (max, sum) per (row, split, head), then
 // one 8-byte arrival ticket per (row, CTA rank).
 size_t mla_ws_bytes(int num_rows, int n_heads, int d_c, int splits) {
@@ -883,9 +850,7 @@ dsa_status launch_mla_tc(const MlaArgs& a, cudaStream_t stream) {
   attr2[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr2;
   cfg.numAttrs = 2;
-  // a launch id for the split arrival tickets: distinct for consecutive launches, never 0
-  static std::atomic<uint32_t> launch_seq{0};
-  do la.launch_id = launch_seq.fetch_add(1u) + 1u; while (la.launch_id == 0u);
+  la.launch_id = next_launch_id();
   cudaError_t e = cudaLaunchKernelEx(&cfg, mla_tc_kernel, la, keys_per_split);
   if (e != cudaSuccess) {
     set_error("mla_tc launch: %s", cudaGetErrorString(e));

@@ -326,3 +326,13 @@ def test_capture_replay_and_two_graphs(N):
         graphs[0].replay(), graphs[1].replay()
     a.check(), b.check()
     assert a.status() == (0, -1)
+
+
+@pytest.mark.parametrize("kw,tc", [(dict(H=128), True), (dict(H=16), True), (dict(H=136), False), (dict(H=8, d_c=64, d_r=16), False),
+                                   (dict(H=128, algo=1), False)])
+def test_which_kernel_runs(N, kw, tc):
+    """The tensor-core kernel takes every row of up to 128 heads of 512 + 64 dims."""
+    c = Case(N, [70, 3], topk=100, seed=12, **kw).build().call()
+    c.algo = N.DSA_ALGO_AUTO if tc else N.DSA_ALGO_SIMT
+    c.check()
+    assert c.ran() & (N.DSA_KERNEL_MLA_SIMT | N.DSA_KERNEL_MLA_INT4_TC) == (N.DSA_KERNEL_MLA_INT4_TC if tc else N.DSA_KERNEL_MLA_SIMT)

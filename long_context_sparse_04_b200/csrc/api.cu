@@ -178,9 +178,6 @@ CacheMap make_map(const dsa_cache* c) {
   return m;
 }
 
-// Heads of the split partials: the kernel over packed rows keeps 128 (fewer are padded).
-int mla_ws_heads(const dsa_dims* d) { return d->mla_dtype == DSA_INT4 && d->n_heads < 128 ? 128 : d->n_heads; }
-
 // Workspace layout (offsets from ws, each 256-byte aligned).
 struct WsPlan {
   size_t status = 0;
@@ -221,9 +218,11 @@ WsPlan plan(const dsa_dims* d, const dsa_rows* r, dsa_op op) {
     off += p.idx_bytes;
   }
   if (need_mla) {
-    p.splits = (op == DSA_OP_DECODE_STEP || op == DSA_OP_SPARSE_MLA) ? mla_tc_splits(rows) : 1;
+    // (the kernel over packed rows merges its splits without scratch)
+    p.splits = (op == DSA_OP_DECODE_STEP || op == DSA_OP_SPARSE_MLA) && d->mla_dtype != DSA_INT4
+                   ? mla_tc_splits(rows) : 1;
     p.mla = off;
-    p.mla_bytes = align_up(mla_ws_bytes(rows, mla_ws_heads(d), d->d_c, p.splits));
+    p.mla_bytes = align_up(mla_ws_bytes(rows, d->n_heads, d->d_c, p.splits));
     off += p.mla_bytes;
   }
   // per-row score histograms of the fused indexer -> top-k (query groups of
@@ -373,8 +372,8 @@ MlaArgs mla_args(const dsa_dims* d, const dsa_rows* r, const dsa_cache* c, const
   a.splits = p.splits;
   a.part_o = at(ws, p.mla);
   a.part_ml = reinterpret_cast<float*>(
-      at(ws, p.mla + (size_t)r->num_rows * p.splits * mla_ws_heads(d) * d->d_c * sizeof(float)));
-  a.part_cnt = reinterpret_cast<unsigned long long*>(a.part_ml + (size_t)r->num_rows * p.splits * mla_ws_heads(d) * 4);
+      at(ws, p.mla + (size_t)r->num_rows * p.splits * d->n_heads * d->d_c * sizeof(float)));
+  a.part_cnt = reinterpret_cast<unsigned long long*>(a.part_ml + (size_t)r->num_rows * p.splits * d->n_heads * 4);
   a.trace = trace_buffer() ? trace_buffer() + kTraceMla : nullptr;
   return a;
 }

@@ -5,7 +5,7 @@
 
 #include <cuda_bf16.h>
 
-#include "dsa_common.cuh"
+#include "dsa_kernels.cuh"
 
 namespace dsa {
 
@@ -48,6 +48,12 @@ __device__ __forceinline__ uint32_t take_ticket(unsigned long long* slot, uint32
   }
   set_status(st, DSA_ERR_TIMEOUT, 29);
   return 0u;
+}
+
+// Profiling stamp: event `ev` of block j in the first cluster's first pair.
+__device__ __forceinline__ void tstamp(long long* tr, uint32_t rank, int ev, int j) {
+  if (tr != nullptr && blockIdx.x < 2 && j < kTraceBlocks)
+    tr[((int)rank * kTraceEvents + ev) * kTraceBlocks + j] = clock64();
 }
 
 uint32_t next_launch_id();

@@ -8,30 +8,38 @@
 // adds no rounding: what is rounded is each softmax weight, to bf16 once for the
 // second product (relative 2^-8 at most, its sum is kept in fp32), and the output.
 //
-// Work unit: (row t, key split), one cluster of two CTAs.  The pair runs every
-// product as one two-CTA tcgen05.mma (M = 128 heads, 64 of them in each CTA), so
-// each CTA has its own heads' logits, softmax state and output rows, and nothing
-// of the softmax crosses between them:
+// Work unit: (row t, key split), one pair of CTAs.  The pair runs every product as
+// two-CTA tcgen05.mma (M = 128 heads, 64 of them in each CTA), so each CTA has its
+// own heads' logits, softmax state and output rows, and nothing of the softmax
+// crosses between them:
 //   S = Q K^T   M=128, N=64 keys, K=576.  CTA r holds the 64 heads' Q and keys
 //               [32r, 32r+32) of the block, all 576 dims.
 //   O += P V    M=128, N=2x256 dims, K=64 keys.  CTA r holds its heads' P and
 //               dims [256r, 256r+256) of all 64 keys.
 // In tensor memory lane l < 64 of a CTA is head l with the first half of N, lane
-// l + 64 the same head with the second half.
+// l + 64 the same head with the second half.  A block of 64 keys takes the tensor
+// cores 1,428 cycles (36 MMAs of 25 cycles, bound by the operands' shared-memory
+// reads, and 8 of 65) against 1,088 at their peak; 128 keys would run the first
+// product at the peak, but two stages of them do not fit beside Q.
 // The two operands overlap in a quarter of the block only, and each CTA decodes
 // both for itself straight from the packed rows: at three instructions a pair of
 // values that is cheaper than an exchange through distributed shared memory.
 //
-// Roles per CTA (672 threads):
-//   warps 0-3    softmax and output: thread (l) = TMEM lane; 32 keys of a head per
-//                block, the two halves of a head share the maximum through shared
+// Roles per CTA (832 threads):
+//   warps 0-7    softmax and output: two threads per TMEM lane, 16 keys of a head
+//                each; a head's four threads share its maximum through shared
 //                memory.  Lazy rescale as in mla_tc.cu.
-//   warps 4-11   decode the keys' tile: packed pieces from global memory to
-//                registers one block ahead, then 16-byte stores, swizzled.
-//   warps 12-19  decode the values' tile, the same way
-//   warp 20      tensor memory; in the pair's first CTA one thread issues the MMAs
-// The tiles have two stages each; S of block j+1 is issued before P V of block j,
-// so that the tensor cores work while the softmax of block j runs.
+//   warps 8-15   decode the keys' tile: packed pieces from global memory to
+//                registers one block ahead, then 16-byte stores, swizzled
+//   warps 16-23  decode the values' tile, the same way
+//   warp 24      tensor memory; in the pair's first CTA one thread issues the MMAs
+//   warp 25      resolves the selection to cache rows, two blocks ahead of the
+//                decoding, and prefetches the rows into L2
+// Tiles, weights and logits have two stages each; S of block j+1 is issued before
+// P V of block j, so that the tensor cores work while the softmax of block j runs.
+//
+// Decode batches split a row's keys over 2 or 4 pairs of one cluster, which merge
+// through distributed shared memory: no scratch in global memory, no arrival order.
 #include "dsa_int4.cuh"
 #include "dsa_kernels.cuh"
 #include "mla_common.cuh"
@@ -44,31 +52,41 @@ constexpr int kDC = 512, kDR = 64, kD = kDC + kDR;
 constexpr Int4Row kRow = int4_row(kDC, kDR);
 constexpr int kBlk = 64, kHalfBlk = 32;
 constexpr int kMaxKeys = 2048;
-constexpr int kKWarp0 = 4, kVWarp0 = 12, kDecWarps = 8, kMmaWarp = 20;
-constexpr int kThreads = 32 * 21;
+constexpr int kMaxPairs = 4;                    // key splits of a row: 1, 2 or 4 (a cluster of 8 CTAs)
+constexpr int kSmWarps = 8, kDecWarps = 8;
+constexpr int kKWarp0 = 8, kVWarp0 = 16, kMmaWarp = 24, kRowWarp = 25;
+constexpr int kThreads = 32 * 26;
+constexpr int kSmThreads = 32 * kSmWarps;
 constexpr int kDecThreads = 2 * kDecWarps * 32;
 constexpr int kQChunks = kD / 64;               // 64-dim SW128 chunks: 8 latent, 1 RoPE
 constexpr uint32_t kColS = 0, kColO = 64, kTmemCols = 512;
 // polls of a bounded wait (20 ms at least; real waits take microseconds)
 constexpr uint32_t kWaitPolls = 1u << 20;
 
-struct __align__(1024) Smem {
+struct Smem {                                   // 1024-byte aligned
   uint8_t q[kQChunks][kHc * 128];               // this CTA's heads
   uint8_t k[2][kQChunks][kHalfBlk * 128];       // its 32 keys, 576 dims
   uint8_t v[2][4][kBlk * 128];                  // 64 keys, its 256 dims
-  uint8_t p[kHc * 128];                         // its heads' weights of 64 keys
-  int32_t rows[kMaxKeys];                       // physical cache row per selected key, -1 = none
+  uint8_t p[2][kHc * 128];                      // its heads' weights of 64 keys
+  float red[2][2][2 * kHc];                     // block maxima, [parity][column half][lane]; the final sums
+  int32_t rows[2][kBlk];                        // physical cache row per key of a block, -1 = none
   uint32_t valid[kMaxKeys / 32];                // per 32 keys: bit i set = key i has a row
-  float red[2][2 * kHc];                        // block maxima by lane; the final sums
-  // waited for by the issuing thread, in the first CTA's shared memory
-  uint64_t q_full, k_full[2], v_full[2], p_full, s_free[2];
+  // waited for by the issuing thread, in the pair's first CTA
+  uint64_t q_full, k_full[2], v_full[2], p_full[2], s_free[2];
   // arrivals of finished products, in both CTAs
   uint64_t s_full[2], pv_done[2];
+  uint64_t rows_full[2], rows_free[2];
   uint64_t drained;
   uint32_t tmem_base;
-  int last_flag;
 };
-static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "shared memory of the attention kernel");
+static_assert(sizeof(Smem) <= 227 * 1024, "shared memory of the attention kernel");
+static_assert(offsetof(Smem, k) % 1024 == 0 && offsetof(Smem, v) % 1024 == 0 && offsetof(Smem, p) % 1024 == 0, "swizzle");
+// The merge of a row's key splits: the split's pair s finishes columns
+// [256 s / S, 256 (s + 1) / S) of every lane and receives them from the other
+// pairs, [source][column / 4][lane] float4, where Q and K lay; then (max, sum) per
+// source and head.
+constexpr size_t kMlOff = 3 * 32768;
+static_assert(kMlOff + kMaxPairs * kHc * sizeof(float2) <= offsetof(Smem, v), "merge layout");
 
 // ---------------------------------------------------------------- two-CTA tcgen05
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* smem_dst, uint32_t ncols) {
@@ -89,65 +107,93 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, 
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
-// Arrive on `bar` of both CTAs when the products issued so far are done.
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+// True in one lane of a converged warp.  The compiler knows that what follows is
+// run by one thread and keeps the descriptors in uniform registers; under
+// `lane == 0` it moved every operand of every MMA there first, and issuing a
+// block's 44 MMAs took 4,800 cycles.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// Arrive on `bar` of the pair's two CTAs (cluster ranks `mask`) when the products
+// issued so far are done.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint16_t mask) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)), "h"((uint16_t)3) : "memory");
+          smem_u32(bar)), "h"(mask) : "memory");
 }
 __device__ __forceinline__ bool wait_local(uint64_t* bar, uint32_t parity, DeviceStatus* st, int site) {
   return mbar_wait(bar, parity, st, site, kWaitPolls);
 }
-// Waits for arrivals of the other CTA too (acquire at cluster scope).
-__device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, DeviceStatus* st, int site) {
-  for (uint32_t i = 0; i < kWaitPolls; ++i)
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-  set_status(st, DSA_ERR_TIMEOUT, site);
-  return false;
+// The same, agreed on by the warp (its lanes go on or leave together).
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, DeviceStatus* st, int site) {
+  return __all_sync(0xffffffffu, wait_local(bar, parity, st, site));
 }
-// One arrival per warp on a barrier of the pair's first CTA.
-__device__ __forceinline__ void warp_arrive_first(uint64_t* bar) {
+// One arrival per warp on a barrier of the pair's first CTA.  What it announces
+// lies in the arriving CTA's own shared or tensor memory and is read by the tensor
+// cores only: fence.proxy.async (stores) or tcgen05.fence (tensor-memory reads),
+// executed before it by every lane, makes that visible to them, so the arrive
+// itself is ordered at CTA scope.  A release at cluster scope would also wait for
+// this thread's global loads in flight: it cost 1,000 cycles an arrive, and a
+// block 5,800 cycles instead of 2,700.
+__device__ __forceinline__ void warp_arrive_first(uint64_t* bar, uint32_t first) {
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive_cluster(bar, 0);
+  if ((threadIdx.x & 31) == 0)
+    asm volatile(
+        "{\n\t.reg .b32 ra;\n\t"
+        "mapa.shared::cluster.u32 ra, %0, %1;\n\t"
+        "mbarrier.arrive.release.cta.shared::cluster.b64 _, [ra];\n\t}" ::"r"(smem_u32(bar)), "r"(first) : "memory");
+}
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 // ---------------------------------------------------------------- MMA issue (first CTA, one thread)
-__device__ __forceinline__ void issue_products(Smem& S, DeviceStatus* status, uint32_t tmem, int nblk) {
+__device__ __forceinline__ void issue_products(Smem& S, const MlaArgs& a, uint32_t tmem, int nblk, uint16_t mask) {
+  DeviceStatus* status = a.status;
   constexpr uint32_t idesc_s = idesc_bf16(kBlk, false);
   constexpr uint32_t idesc_pv = idesc_bf16(256, true);
-  bool ok = wait_pair(&S.q_full, 0, status, 41);
-  const uint32_t qa = smem_u32(S.q), pa = smem_u32(S.p);
+  bool ok = wait_local(&S.q_full, 0, status, 41);
+  // descriptors: a byte offset within the tile adds offset >> 4 to the address field
+  const uint64_t qd = sdesc_sw128(smem_u32(S.q), 16, 1024), pd = sdesc_sw128(smem_u32(S.p), 16, 1024);
+  const uint64_t kd0 = sdesc_sw128(smem_u32(S.k[0]), 16, 1024);
+  const uint64_t vd0 = sdesc_sw128(smem_u32(S.v[0]), kBlk * 128, 1024);
   for (int j = 0; ok && j <= nblk; ++j) {
     if (j < nblk) {
       const int b = j & 1;
-      ok = wait_pair(&S.k_full[b], (j >> 1) & 1, status, 42) && wait_pair(&S.s_free[b], ((j >> 1) & 1) ^ 1, status, 43);
+      ok = wait_local(&S.k_full[b], (j >> 1) & 1, status, 42) && wait_local(&S.s_free[b], ((j >> 1) & 1) ^ 1, status, 43);
       if (!ok) break;
-      fence_proxy_async_smem();
       tc_fence_after();
-      const uint32_t ka = smem_u32(S.k[b]);
+      const uint64_t kd = kd0 + (uint64_t)(b * (sizeof(S.k[0]) >> 4));
+      const uint32_t d = tmem + kColS + b * 32;
 #pragma unroll
       for (int ch = 0; ch < kQChunks; ++ch)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_bf16_pair(tmem + kColS + b * 32, sdesc_sw128(qa + ch * kHc * 128 + 32 * kk, 16, 1024),
-                        sdesc_sw128(ka + ch * kHalfBlk * 128 + 32 * kk, 16, 1024), idesc_s, (ch | kk) != 0);
-      mma_commit_pair(&S.s_full[b]);
+          mma_bf16_pair(d, qd + (ch * kHc * 128 + 32 * kk >> 4), kd + (ch * kHalfBlk * 128 + 32 * kk >> 4), idesc_s,
+                        (ch | kk) != 0);
+      mma_commit_pair(&S.s_full[b], mask);
+      tstamp(a.trace, 0, 2, j);
     }
     if (j >= 1) {
       const int jj = j - 1, b = jj & 1;
-      ok = wait_pair(&S.v_full[b], (jj >> 1) & 1, status, 44) && wait_pair(&S.p_full, jj & 1, status, 45);
+      ok = wait_local(&S.v_full[b], (jj >> 1) & 1, status, 44) && wait_local(&S.p_full[b], (jj >> 1) & 1, status, 45);
       if (!ok) break;
-      fence_proxy_async_smem();
       tc_fence_after();
-      const uint32_t va = smem_u32(S.v[b]);
+      const uint64_t vd = vd0 + (uint64_t)(b * (sizeof(S.v[0]) >> 4));
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
         for (int n = 0; n < 2; ++n)
-          mma_bf16_pair(tmem + kColO + n * 128, sdesc_sw128(pa + 32 * kk, 16, 1024),
-                        sdesc_sw128(va + n * 2 * kBlk * 128 + kk * 16 * 128, kBlk * 128, 1024), idesc_pv,
-                        (jj | kk) != 0);
-      mma_commit_pair(&S.pv_done[b]);
+          mma_bf16_pair(tmem + kColO + n * 128, pd + b * (sizeof(S.p[0]) >> 4) + (32 * kk >> 4),
+                        vd + (n * 2 * kBlk * 128 + kk * 16 * 128 >> 4), idesc_pv, (jj | kk) != 0);
+      mma_commit_pair(&S.pv_done[b], mask);
+      tstamp(a.trace, 0, 3, jj);
     }
   }
   // every product issued is done before the pair's shared and tensor memory go
@@ -156,85 +202,178 @@ __device__ __forceinline__ void issue_products(Smem& S, DeviceStatus* status, ui
   wait_local(&S.drained, 0, status, 46);
 }
 
+// ---------------------------------------------------------------- the selection
+// One warp turns the selection into cache rows, two keys of a block per lane: the
+// loads of a block's block-table entries and of the next block's positions are in
+// flight while the block before is handed over.
+__device__ __forceinline__ void resolve_rows(Smem& S, const MlaArgs& a, int t, int seq, int klen, int k0, int nvalid,
+                                             int nblk, uint32_t rank) {
+  const int lane = threadIdx.x & 31;
+  const int32_t* idx = a.idx + (int64_t)t * a.topk + k0;
+  const CacheMap& m = a.map;
+  const uint8_t* latent = static_cast<const uint8_t*>(a.latent);
+  const int32_t* table = m.block_table ? m.block_table + (int64_t)seq * m.max_pages_per_seq : nullptr;
+  const int64_t start = !m.block_table && m.seq_start ? (int64_t)__ldg(m.seq_start + seq) : 0;
+  const auto position = [&](int j, int u) {
+    const int i = j * kBlk + 32 * u + lane;
+    const int s = i < nvalid ? __ldg(idx + i) : -1;
+    return s < klen ? s : -1;
+  };
+  const auto page_of = [&](int s) { return m.page_shift >= 0 ? s >> m.page_shift : s / m.page_size; };
+  // the block-table entry of position s (-1: none)
+  const auto entry = [&](int s) {
+    if (s < 0 || table == nullptr) return -1;
+    const int pg = page_of(s);
+    if (pg >= m.max_pages_per_seq) {
+      set_status(a.status, DSA_ERR_OUT_OF_RANGE, s);
+      return -1;
+    }
+    const int p = __ldg(table + pg);
+    return p;
+  };
+  const auto row_of = [&](int s, int e) {
+    if (s < 0) return -1;
+    if (table != nullptr) {
+      const int pg = page_of(s);
+      if (pg >= m.max_pages_per_seq) return -1;
+      if (e < 0 || e >= m.num_pages) {
+        set_status(a.status, DSA_ERR_OUT_OF_RANGE, e);
+        return -1;
+      }
+      return (int)((int64_t)e * m.page_size + (s - pg * m.page_size));
+    }
+    const int64_t r = start + s;
+    if (r < 0 || r >= m.num_tokens) {
+      set_status(a.status, DSA_ERR_OUT_OF_RANGE, s);
+      return -1;
+    }
+    return (int)r;
+  };
+  int s0[2], s1[2], e0[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) s0[u] = position(0, u);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    s1[u] = position(1, u);
+    e0[u] = entry(s0[u]);
+  }
+  for (int j = 0; j < nblk; ++j) {
+    int s2[2], e1[2], row[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      s2[u] = position(j + 2, u);
+      e1[u] = entry(s1[u]);
+    }
+    if (!wait_warp(&S.rows_free[j & 1], ((j >> 1) & 1) ^ 1, a.status, 53)) break;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      row[u] = row_of(s0[u], e0[u]);
+      S.rows[j & 1][32 * u + lane] = row[u];
+      const uint32_t bits = __ballot_sync(0xffffffffu, row[u] >= 0);
+      if (lane == 0) S.valid[2 * j + u] = bits;
+      s0[u] = s1[u];
+      s1[u] = s2[u];
+      e0[u] = e1[u];
+    }
+    warp_arrive(&S.rows_full[j & 1]);
+    // each CTA of the pair prefetches half of the block's rows
+    const int mine = rank ? row[1] : row[0];
+    if (mine >= 0)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(latent + (int64_t)mine * kRow.bytes), "n"(kRow.bytes)
+                   : "memory");
+  }
+}
+
 // ---------------------------------------------------------------- decoding
-// A warp's share of one block: two pieces of 32 dims of a key per lane.  Eight
+// A warp's share of one block: two pieces of 32 dims of one key per lane.  Eight
 // neighbouring lanes take eight keys (their 16-byte stores fall into distinct
 // banks of the swizzled tile), the four lane groups four neighbouring pieces (64
 // bytes of codes of one key: two whole sectors).
+//   keys' tile:   warp w takes keys 8 (w % 4).., pieces 4 (w / 4).. and 8 further on
+//   values' tile: warp w takes keys 8 w..,       pieces 0.. and 4 further on
 template <bool kV>
 struct Decoder {
-  uint4 codes[2];
-  uint32_t scales[2];
-  uint4 rope;
+  static constexpr int kChunk = (kV ? kBlk : kHalfBlk) * 128;    // bytes of 64 dims of the tile
+  static constexpr int kNext = kV ? 4 : 8;                       // pieces from a lane's first to its second
+  struct Pieces {
+    uint4 codes[2], rope;
+    uint32_t scales[2];
+  };
+  int key, src_codes, src_scales, rope_key, rope_src;            // of the lane: key in the block, byte offsets in the row
+  uint32_t dst[4], rope_dst;                                     // shared-memory offsets in a tile
 
-  static __device__ __forceinline__ void place(int wt, int i, int& key, int& piece) {
-    const int lane = threadIdx.x & 31, task = wt + kDecWarps * i;
-    key = (kV ? task & 7 : task & 3) * 8 + (lane & 7);
-    piece = (kV ? task >> 3 : task >> 2) * 4 + (lane >> 3);
-  }
-  // Loads block j's packed pieces (zeros for a key without a row).
-  __device__ __forceinline__ void load(const Smem& S, const uint8_t* latent, int j, int wt, uint32_t rank) {
-    const int32_t* rows = S.rows + j * kBlk + (kV ? 0 : kHalfBlk * (int)rank);
+  __device__ __forceinline__ Decoder(int wt, uint32_t rank) {
+    const int lane = threadIdx.x & 31, low = lane & 7, grp = lane >> 3;
+    const int in_tile = (kV ? wt : wt & 3) * 8 + low, piece = (kV ? 0 : (wt >> 2) * 4) + grp;
+    key = in_tile + (kV ? 0 : kHalfBlk * (int)rank);
+    src_codes = 16 * (piece + (kV ? 8 * (int)rank : 0));
+    src_scales = kRow.scale + 2 * (piece + (kV ? 8 * (int)rank : 0));
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      int key, piece;
-      place(wt, i, key, piece);
-      if (kV) piece += 8 * (int)rank;
-      const int row = rows[key];
+    for (int e = 0; e < 4; ++e) dst[e] = (piece >> 1) * kChunk + sw128_off(in_tile, (piece & 1) * 4 + e);
+    const int kt = wt * 32 + lane;                               // RoPE: 32 keys x 8 pieces, one per thread
+    rope_key = (kt >> 3) + kHalfBlk * (int)rank;
+    rope_src = kRow.rope + 16 * (kt & 7);
+    rope_dst = 8 * kChunk + sw128_off(kt >> 3, kt & 7);
+  }
+  // Loads a block's packed pieces (zeros for a key without a row).
+  __device__ __forceinline__ void load(Pieces& x, const int32_t* rows, const uint8_t* latent) const {
+    const int row = rows[key];
+    const int rrow = kV ? -1 : rows[rope_key];
+    x.codes[0] = x.codes[1] = x.rope = make_uint4(0u, 0u, 0u, 0u);
+    x.scales[0] = x.scales[1] = 0u;
+    if (row >= 0) {
       const uint8_t* src = latent + (int64_t)row * kRow.bytes;
-      codes[i] = make_uint4(0u, 0u, 0u, 0u);
-      scales[i] = 0u;
-      if (row >= 0) {
-        codes[i] = __ldg(reinterpret_cast<const uint4*>(src) + piece);
-        scales[i] = __ldg(reinterpret_cast<const unsigned short*>(src + kRow.scale) + piece);
-      }
+      x.codes[0] = __ldg(reinterpret_cast<const uint4*>(src + src_codes));
+      x.codes[1] = __ldg(reinterpret_cast<const uint4*>(src + src_codes + 16 * kNext));
+      x.scales[0] = __ldg(reinterpret_cast<const unsigned short*>(src + src_scales));
+      x.scales[1] = __ldg(reinterpret_cast<const unsigned short*>(src + src_scales + 2 * kNext));
     }
-    if (!kV) {
-      const int kt = wt * 32 + (threadIdx.x & 31), row = rows[kt >> 3];
-      rope = make_uint4(0u, 0u, 0u, 0u);
-      if (row >= 0)
-        rope = __ldg(reinterpret_cast<const uint4*>(latent + (int64_t)row * kRow.bytes + kRow.rope) + (kt & 7));
-    }
+    if (!kV && rrow >= 0) x.rope = __ldg(reinterpret_cast<const uint4*>(latent + (int64_t)rrow * kRow.bytes + rope_src));
   }
-  __device__ __forceinline__ void store(uint8_t* tile, int wt) const {
-    constexpr int kChunk = (kV ? kBlk : kHalfBlk) * 128;
+  __device__ __forceinline__ void store(const Pieces& x, uint8_t* tile) const {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      int key, piece;
-      place(wt, i, key, piece);
-      uint8_t* dst = tile + (piece >> 1) * kChunk;
-      const int p0 = (piece & 1) * 4;
-      const ScalePair s0 = scale_pair(scales[i] & 0xFFu), s1 = scale_pair(scales[i] >> 8);
-      *reinterpret_cast<uint4*>(dst + sw128_off(key, p0)) = decode_word(codes[i].x, s0);
-      *reinterpret_cast<uint4*>(dst + sw128_off(key, p0 + 1)) = decode_word(codes[i].y, s0);
-      *reinterpret_cast<uint4*>(dst + sw128_off(key, p0 + 2)) = decode_word(codes[i].z, s1);
-      *reinterpret_cast<uint4*>(dst + sw128_off(key, p0 + 3)) = decode_word(codes[i].w, s1);
+      uint8_t* t = tile + i * (kNext / 2) * kChunk;
+      const ScalePair s0 = scale_pair(x.scales[i] & 0xFFu), s1 = scale_pair(x.scales[i] >> 8);
+      *reinterpret_cast<uint4*>(t + dst[0]) = decode_word(x.codes[i].x, s0);
+      *reinterpret_cast<uint4*>(t + dst[1]) = decode_word(x.codes[i].y, s0);
+      *reinterpret_cast<uint4*>(t + dst[2]) = decode_word(x.codes[i].z, s1);
+      *reinterpret_cast<uint4*>(t + dst[3]) = decode_word(x.codes[i].w, s1);
     }
-    if (!kV) {
-      const int kt = wt * 32 + (threadIdx.x & 31);
-      *reinterpret_cast<uint4*>(tile + 8 * kChunk + sw128_off(kt >> 3, kt & 7)) = rope;
-    }
+    if (!kV) *reinterpret_cast<uint4*>(tile + rope_dst) = x.rope;
   }
 };
 
 template <bool kV>
-__device__ __forceinline__ void decode_blocks(Smem& S, const MlaArgs& a, int nblk, uint32_t rank, int wt) {
+__device__ __forceinline__ void decode_blocks(Smem& S, const MlaArgs& a, int nblk, uint32_t rank, uint32_t first, int wt) {
   const uint8_t* latent = static_cast<const uint8_t*>(a.latent);
-  Decoder<kV> cur, nxt;
-  cur.load(S, latent, 0, wt, rank);
+  const Decoder<kV> dec(wt, rank);
+  typename Decoder<kV>::Pieces even, odd;         // the packed pieces of even and odd blocks
+  const bool stamp = wt == 0 && (threadIdx.x & 31) == 0;
+  const auto fetch = [&](int j, typename Decoder<kV>::Pieces& x) {
+    if (!wait_warp(&S.rows_full[j & 1], (j >> 1) & 1, a.status, 54)) return false;
+    dec.load(x, S.rows[j & 1], latent);
+    warp_arrive(&S.rows_free[j & 1]);
+    return true;
+  };
+  bool ok = fetch(0, even);
   cp_async_wait_all();                            // this thread's pieces of Q
   fence_proxy_async_smem();
-  warp_arrive_first(&S.q_full);
-  for (int j = 0; j < nblk; ++j) {
+  warp_arrive_first(&S.q_full, first);
+  const auto block = [&](int j, const typename Decoder<kV>::Pieces& now, typename Decoder<kV>::Pieces& next) {
     const int b = j & 1;
-    if (j + 1 < nblk) nxt.load(S, latent, j + 1, wt, rank);
+    if (j + 1 < nblk && !fetch(j + 1, next)) return false;
     // the stage is free once the products of block j-2 have read it
-    if (!wait_local(kV ? &S.pv_done[b] : &S.s_full[b], ((j >> 1) & 1) ^ 1, a.status, kV ? 48 : 47)) break;
-    cur.store(kV ? S.v[b][0] : S.k[b][0], wt);
+    if (!wait_warp(kV ? &S.pv_done[b] : &S.s_full[b], ((j >> 1) & 1) ^ 1, a.status, kV ? 48 : 47)) return false;
+    if (stamp) tstamp(a.trace, rank, kV ? 7 : 5, j);
+    dec.store(now, kV ? S.v[b][0] : S.k[b][0]);
     fence_proxy_async_smem();                     // generic stores -> tensor cores
-    warp_arrive_first(kV ? &S.v_full[b] : &S.k_full[b]);
-    cur = nxt;
-  }
+    warp_arrive_first(kV ? &S.v_full[b] : &S.k_full[b], first);
+    if (stamp) tstamp(a.trace, rank, kV ? 1 : 0, j);
+    return true;
+  };
+  for (int j = 0; ok && j < nblk; j += 2)
+    ok = block(j, even, odd) && (j + 1 >= nblk || block(j + 1, odd, even));
 }
 
 // 32 columns of this thread's lane of O (zeros when no product was issued).
@@ -248,31 +387,124 @@ __device__ __forceinline__ void load_o32(uint32_t taddr, bool empty, float (&o)[
   tmem_wait_ld();
 }
 
-__global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(MlaArgs a, int keys_per_split) {
+// Softmax state of a thread: lane l of tensor memory (head l % 64, key half l / 64),
+// columns [16 cw, 16 cw + 16) of the lane's 32.
+struct Softmax {
+  float m = -INFINITY, sum = 0.f;                 // running maximum (log2 domain) and this thread's sum
+  bool dead = false;                              // a wait ran out
+
+  // One block; false when the warpgroups leave together because a wait ran out (a
+  // dead thread goes on to the next block's barrier, so that every barrier and
+  // collective access stays uniform).
+  __device__ __forceinline__ bool block(Smem& S, const MlaArgs& a, uint32_t tmem_lane, int j, float c, uint32_t rank,
+                                        uint32_t first) {
+    const int b = j & 1, l = threadIdx.x & 127, cw = threadIdx.x >> 7, half = l >> 6, hl = l & 63;
+    dead = dead || !wait_local(&S.s_full[b], (j >> 1) & 1, a.status, 49);
+    tc_fence_after();
+    if (threadIdx.x == 0) tstamp(a.trace, rank, 4, j);
+    float s[16];
+    tmem_ld16(tmem_lane + kColS + b * 32 + 16 * cw, *reinterpret_cast<uint32_t(*)[16]>(&s[0]));
+    tmem_wait_ld();
+    tc_fence_before();
+    warp_arrive_first(&S.s_free[b], first);
+    // masked keys are -inf (whole words of a full block need no test)
+    const uint32_t mask = S.valid[2 * j + half] >> (16 * cw);
+    if ((mask & 0xFFFFu) != 0xFFFFu) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (!((mask >> i) & 1u)) s[i] = -INFINITY;
+    }
+    float pm[4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) pm[i & 3] = (i < 4) ? s[i] : fmaxf(pm[i & 3], s[i]);
+    const float mh = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
+    S.red[b][cw][l] = mh;
+    if (named_bar_or(1, kSmThreads, dead)) { dead = true; return false; }
+    // the four threads of a head take the same maximum
+    const float mb = c * fmaxf(fmaxf(mh, S.red[b][cw][l ^ 64]), fmaxf(S.red[b][cw ^ 1][l], S.red[b][cw ^ 1][l ^ 64]));
+    // lazy rescale: P stays <= 2^8.  Warp-uniform (tensor-memory access is collective)
+    const bool need = mb > m + kRescale;
+    if (__any_sync(0xffffffffu, need)) {
+      const float m_new = need ? mb : m;
+      const float alpha = need ? (m == -INFINITY ? 0.f : exp2f(m - m_new)) : 1.f;
+      if (j > 0) {
+        dead = dead || !wait_local(&S.pv_done[b ^ 1], ((j - 1) >> 1) & 1, a.status, 50);
+        tc_fence_after();
+#pragma unroll 1
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t o[32];
+          const uint32_t col = tmem_lane + kColO + 128 * cw + 32 * cc;
+          tmem_ld32(col, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          tmem_st32(col, o);
+        }
+        tmem_wait_st();
+      }
+      sum *= alpha;
+      m = m_new;
+    }
+    // p = 2^(c s - m); while no key of the head has been visible m counts as 0
+    const float mu = (m == -INFINITY) ? 0.f : -m;
+    uint32_t p2[8];
+    float ls[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float p0 = ex2_approx(fmaf(s[2 * i], c, mu));
+      const float p1 = ex2_approx(fmaf(s[2 * i + 1], c, mu));
+      ls[0] += p0;
+      ls[1] += p1;
+      p2[i] = pack_bf16x2(p0, p1);
+    }
+    sum += ls[0] + ls[1];
+    // the weights' tile is free once P V of block j-2 is done
+    dead = dead || !wait_local(&S.pv_done[b], ((j >> 1) & 1) ^ 1, a.status, 51);
+    uint8_t* p = S.p[b];
+    *reinterpret_cast<uint4*>(p + sw128_off(hl, 4 * half + 2 * cw)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+    *reinterpret_cast<uint4*>(p + sw128_off(hl, 4 * half + 2 * cw + 1)) = make_uint4(p2[4], p2[5], p2[6], p2[7]);
+    fence_proxy_async_smem();
+    tc_fence_before();
+    warp_arrive_first(&S.p_full[b], first);
+    if (threadIdx.x == 0) tstamp(a.trace, rank, 6, j);
+    return true;
+  }
+};
+
+// S: key splits of a row = pairs of a cluster.
+template <int kSplits>
+__global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(MlaArgs a) {
   extern __shared__ __align__(1024) uint8_t smraw[];
-  Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
-  const int unit = blockIdx.x >> 1;
-  const int t = unit / a.splits, sp = unit % a.splits;
+  Smem& S = *reinterpret_cast<Smem*>(smraw);
+  const int warp = threadIdx.x >> 5;
+  const uint32_t crank = cluster_ctarank(), rank = crank & 1u, first = crank & ~1u;
+  const int sp = (int)(crank >> 1);
+  const int t = blockIdx.x / (2 * kSplits);
   pdl_launch_dependents();
 
   // setup that reads no input memory overlaps the predecessor's tail
   if (threadIdx.x == 0) {
     mbar_init(&S.q_full, 2 * 2 * kDecWarps);
-    mbar_init(&S.p_full, 2 * 4);
     mbar_init(&S.drained, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.k_full[i], 2 * kDecWarps);
       mbar_init(&S.v_full[i], 2 * kDecWarps);
-      mbar_init(&S.s_free[i], 2 * 4);
+      mbar_init(&S.p_full[i], 2 * kSmWarps);
+      mbar_init(&S.s_free[i], 2 * kSmWarps);
       mbar_init(&S.s_full[i], 1);
       mbar_init(&S.pv_done[i], 1);
+      mbar_init(&S.rows_full[i], 1);
+      mbar_init(&S.rows_free[i], 2 * kDecWarps);
     }
     fence_mbar_init();
   }
   __syncwarp();
   if (warp == kMmaWarp) tmem_alloc_pair(&S.tmem_base, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_sync();                       // the pair's barriers are initialised
+  const uint32_t tmem = S.tmem_base;
   pdl_wait();
   trace_kernel(a.status, DSA_KERNEL_MLA_INT4_TC);
   const int klen = a.row_klen[t];
@@ -280,22 +512,23 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(MlaArgs a, int
   const bool known = (seq >= 0 && seq < a.num_seqs) || !a.map.uses_seq();
   if (!known && klen > 0 && threadIdx.x == 0) set_status(a.status, DSA_ERR_OUT_OF_RANGE, t);
   const int nsel = known ? min(klen, a.topk) : 0;
+  // whole blocks per split, shared out over what the row really selects
+  const int keys_per_split = (max(nsel, 0) + kSplits * kBlk - 1) / (kSplits * kBlk) * kBlk;
   const int k0 = sp * keys_per_split;
   const int nvalid = max(0, min(nsel - k0, keys_per_split));
   const int nblk = (nvalid + kBlk - 1) / kBlk;
-  {
-    constexpr int kPer = (kMaxKeys + kThreads - 1) / kThreads;
-    const int32_t* idx = a.idx + (int64_t)t * a.topk + k0;
-    int sv[kPer];
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      const int i = threadIdx.x + u * kThreads;
-      sv[u] = i < nvalid ? __ldg(idx + i) : -1;
-    }
-    // Q lands while the selection is resolved; heads beyond H are zeros
-    const int g = threadIdx.x - 32 * kKWarp0;
-    if (nblk > 0 && g >= 0 && g < kDecThreads) {
-      const int h0 = kHc * (int)rank;
+  const bool empty = nblk == 0;
+  Softmax sm;
+
+  if (warp == kMmaWarp) {
+    if (rank == 0 && !empty && elect_one()) issue_products(S, a, tmem, nblk, (uint16_t)(3u << first));
+    __syncwarp();
+  } else if (warp == kRowWarp) {
+    if (!empty) resolve_rows(S, a, t, seq, klen, k0, nvalid, nblk, rank);
+  } else if (warp >= kKWarp0) {
+    if (!empty) {
+      // Q lands while the selection is resolved; heads beyond H are zeros
+      const int g = threadIdx.x - 32 * kKWarp0, h0 = kHc * (int)rank;
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)t * a.n_heads * kD;
 #pragma unroll
       for (int i = 0; i < kHc * kD / 8 / kDecThreads; ++i) {
@@ -303,229 +536,149 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(MlaArgs a, int
         const bool in = h0 + h < a.n_heads;
         cp_async_16_zfill(S.q[c >> 3] + sw128_off(h, c & 7), q + (int64_t)(in ? h0 + h : 0) * kD + 8 * c, in);
       }
+      if (warp >= kVWarp0) decode_blocks<true>(S, a, nblk, rank, first, warp - kVWarp0);
+      else decode_blocks<false>(S, a, nblk, rank, first, warp - kKWarp0);
     }
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      const int i = threadIdx.x + u * kThreads;
-      int row = -1;
-      if (i < nblk * kBlk) {
-        const int sk = sv[u];
-        if (sk >= 0 && sk < klen) {
-          bool ok = true;
-          const int64_t r = a.map.row(seq, sk, a.status, &ok);
-          row = ok ? (int32_t)r : -1;
-        }
-        S.rows[i] = row;
-      }
-      const uint32_t bits = __ballot_sync(0xffffffffu, row >= 0);
-      if (lane == 0 && i < nblk * kBlk) S.valid[i >> 5] = bits;
+  } else {
+    const float c = a.sm_scale * kLog2e;
+    const uint32_t tmem_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    for (int j = 0; j < nblk; ++j)
+      if (!sm.block(S, a, tmem_lane, j, c, rank, first)) break;
+    if (!sm.dead && !empty) {
+      sm.dead = !wait_local(&S.pv_done[(nblk - 1) & 1], ((nblk - 1) >> 1) & 1, a.status, 52);
+      tc_fence_after();
     }
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  cluster_sync();                       // the pair's barriers are initialised
-  const uint32_t tmem = S.tmem_base;
-
-  if (warp == kMmaWarp) {
-    if (rank == 0 && lane == 0 && nblk > 0) issue_products(S, a.status, tmem, nblk);
-    __syncwarp();
-  } else if (warp >= kVWarp0) {
-    if (nblk > 0) decode_blocks<true>(S, a, nblk, rank, warp - kVWarp0);
-  } else if (warp >= kKWarp0) {
-    if (nblk > 0) decode_blocks<false>(S, a, nblk, rank, warp - kKWarp0);
-  } else {
-    // -------------------------------------------------- softmax and output (128 threads)
-    const int l = threadIdx.x, half = l >> 6, hl = l & 63;
-    const int head = kHc * (int)rank + hl;
-    const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
-    const float c = a.sm_scale * kLog2e;
-    float m_used = -INFINITY, sum = 0.f;
-    // a wait that runs out marks the thread dead; the loop is left together
-    bool dead = false;
-    for (int j = 0; j < nblk; ++j) {
-      const int b = j & 1;
-      dead = dead || !wait_local(&S.s_full[b], (j >> 1) & 1, a.status, 49);
-      tc_fence_after();
-      float s[32];
-      tmem_ld32(tmem + lane_off + kColS + b * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-      tmem_wait_ld();
-      tc_fence_before();
-      warp_arrive_first(&S.s_free[b]);
-      // logits in the log2 domain; masked keys are -inf
-      const uint32_t mask = S.valid[2 * j + half];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) s[i] *= c;
-      if (mask != 0xFFFFFFFFu) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (!((mask >> i) & 1u)) s[i] = -INFINITY;
-      }
-      float pm[8];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) pm[i & 7] = (i < 8) ? s[i] : fmaxf(pm[i & 7], s[i]);
-      const float mh = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])),
-                             fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7])));
-      S.red[b][l] = mh;
-      if (named_bar_or(1, 128, dead)) { dead = true; break; }
-      const float mb = fmaxf(mh, S.red[b][l ^ 64]);
-      // lazy rescale: P stays <= 2^8.  Warp-uniform; a head's two lanes decide alike
-      const bool need = mb > m_used + kRescale;
-      if (__any_sync(0xffffffffu, need)) {
-        const float m_new = need ? mb : m_used;
-        const float alpha = need ? (m_used == -INFINITY ? 0.f : exp2f(m_used - m_new)) : 1.f;
-        if (j > 0) {
-          dead = dead || !wait_local(&S.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, a.status, 50);
-          tc_fence_after();
+  // The row's output.  With key splits the pairs of the cluster first exchange what
+  // they hold: every pair's products are done at the first barrier, so the tiles
+  // may be overwritten; at the second everything has arrived.
+  if (kSplits > 1) {
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+  }
+  const int l = threadIdx.x & 127, cw = threadIdx.x >> 7, half = l >> 6, hl = l & 63;
+  const bool out_warp = warp < kSmWarps;
+  const uint32_t o_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColO;
+  bool fail = false;
+  float lt = 0.f;
+  if (out_warp) {
+    // the head's sum over its four threads; a wait that ran out anywhere fails the CTA
+    named_bar_sync(1, kSmThreads);
+    S.red[0][cw][l] = sm.sum;
+    fail = named_bar_or(1, kSmThreads, sm.dead);
+    lt = (S.red[0][0][hl] + S.red[0][1][hl]) + (S.red[0][0][hl + 64] + S.red[0][1][hl + 64]);
+    if (fail) lt = __int_as_float(0x7FC00000);    // marks the row for the other pairs too
+  }
+  constexpr int kCols = 256 / kSplits;            // columns of each lane that a pair finishes
+  if (kSplits > 1) {
+    if (out_warp) {
 #pragma unroll 1
-          for (int cc = 0; cc < 8; ++cc) {
-            uint32_t o[32];
-            const uint32_t col = tmem + lane_off + kColO + 32 * cc;
-            tmem_ld32(col, o);
-            tmem_wait_ld();
+      for (int cc = 0; cc < 4; ++cc) {            // this thread's half of the columns, 32 at a time
+        const int col = 128 * cw + 32 * cc, to = col / kCols;
+        if (to == sp) continue;
+        float o[32];
+        load_o32(o_lane + col, empty || fail, o);
+        const uint32_t peer = (uint32_t)(2 * to) + rank;
+        const int slot = sp < to ? sp : sp - 1;   // the receiver's other pairs in order
+        const uint32_t dst = mapa(smraw + (size_t)slot * kCols * 512 + (size_t)((col - to * kCols) / 4 * 128 + l) * 16, peer);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st32(col, o);
-          }
-          tmem_wait_st();
+        for (int i = 0; i < 8; ++i)
+          st_dsmem_v4(dst + i * 128 * 16, __float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
+                      __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3]));
+      }
+      if (cw == 0 && half == 0) {
+#pragma unroll
+        for (int to = 0; to < kSplits; ++to) {
+          const uint32_t dst = mapa(smraw + kMlOff + (size_t)(sp * kHc + hl) * sizeof(float2), (uint32_t)(2 * to) + rank);
+          st_dsmem_u32(dst, __float_as_uint(sm.m));
+          st_dsmem_u32(dst + 4, __float_as_uint(lt));
         }
-        sum *= alpha;
-        m_used = m_new;
       }
-      // p = 2^(z - m); while no key of the head has been visible m counts as 0
-      const float mu = (m_used == -INFINITY) ? 0.f : m_used;
-      uint32_t p2[16];
-      float ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float p0 = ex2_approx(s[2 * i] - mu);
-        const float p1 = ex2_approx(s[2 * i + 1] - mu);
-        ls[i & 3] += p0 + p1;
-        p2[i] = pack_bf16x2(p0, p1);
-      }
-      sum += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-      // the weights' tile is free once P V of the block before is done
-      if (j > 0) dead = dead || !wait_local(&S.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, a.status, 51);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4*>(S.p + sw128_off(hl, 4 * half + i)) =
-            make_uint4(p2[4 * i], p2[4 * i + 1], p2[4 * i + 2], p2[4 * i + 3]);
-      fence_proxy_async_smem();
-      tc_fence_before();
-      warp_arrive_first(&S.p_full);
     }
-    if (!dead && nblk > 0) {
-      dead = !wait_local(&S.pv_done[(nblk - 1) & 1], ((nblk - 1) >> 1) & 1, a.status, 52);
-      tc_fence_after();
-    }
-    // the head's sum over its two lanes; a wait that ran out anywhere fails the CTA
-    named_bar_sync(1, 128);
-    S.red[0][l] = sum;
-    const bool fail = named_bar_or(1, 128, dead);
-    const float lt = S.red[0][hl] + S.red[0][hl + 64];
-    const bool empty = nblk == 0;
-    const int heads_here = max(0, min(kHc, a.n_heads - kHc * (int)rank));
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((int64_t)t * a.n_heads + kHc * (int)rank) * kDC;
-    if (fail) {
-      // recorded in the status word: zeros
-      for (int i = l; i < heads_here * (kDC / 8); i += 128) reinterpret_cast<uint4*>(out)[i] = make_uint4(0u, 0u, 0u, 0u);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+  }
+  if (out_warp) {
+    // out = sum_s w_s O_s / sum_s w_s l_s,  w_s = 2^(m_s - max m), splits in order
+    float w[kSplits], M = sm.m, L = lt;
+    if (kSplits == 1) {
+      w[0] = 1.f;
     } else {
-      // the finished rows go through shared memory (the values' tiles, idle now) so
-      // that global writes are whole rows: 64 heads x 64 pieces of 16 bytes, piece
-      // c of head h at c ^ (h % 32)
-      uint8_t* stg = S.v[0][0];
-      const auto stage = [&](const float (&o)[32], int cc, float inv) {
+      const float2* ml = reinterpret_cast<const float2*>(smraw + kMlOff);
+      M = -INFINITY;
+      L = 0.f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<uint4*>(stg + hl * 1024 + (((32 * half + 4 * cc + q) ^ (hl & 31)) << 4)) = pack8(&o[8 * q], inv);
-      };
-      bool write_out = true;
-      if (a.splits == 1) {
-        const float inv = lt > 0.f ? 1.f / lt : 0.f;
+      for (int s2 = 0; s2 < kSplits; ++s2) M = fmaxf(M, ml[s2 * kHc + hl].x);
+#pragma unroll
+      for (int s2 = 0; s2 < kSplits; ++s2) {
+        const float2 v = ml[s2 * kHc + hl];
+        w[s2] = v.x == -INFINITY ? 0.f : exp2f(v.x - M);
+        L += v.x == -INFINITY ? 0.f * v.y : w[s2] * v.y;      // NaN of a failed pair stays
+      }
+    }
+    const bool bad = L != L;
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    // Finished rows go through shared memory (the values' tiles, idle now) so that
+    // global writes are whole segments: 64 heads x 64 pieces of 16 bytes, piece c of
+    // head h at c ^ (h % 32).
+    uint8_t* stg = S.v[0][0];
+    constexpr int kMine = kCols / 2;              // columns of this thread: 128, 64 or 32
 #pragma unroll 1
-        for (int cc = 0; cc < 8; ++cc) {
-          float o[32];
-          load_o32(tmem + lane_off + kColO + 32 * cc, empty, o);
-          stage(o, cc, inv);
-        }
-        if (a.lse && half == 0 && head < a.n_heads)
-          a.lse[(int64_t)t * a.n_heads + head] = lt > 0.f ? (m_used + log2f(lt)) * kLn2 : -INFINITY;
+    for (int cc = 0; cc < kMine / 32; ++cc) {
+      const int col = sp * kCols + kMine * cw + 32 * cc;
+      float o[32];
+      if (bad) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = 0.f;
       } else {
-        // key splits: publish O and (max, sum); the row's last split to arrive (per
-        // CTA rank) merges them in split order:
-        //   out = sum_s w_s O_s / sum_s w_s l_s,  w_s = 2^(m_s - max m)
-        float4* po = reinterpret_cast<float4*>(a.part_o);
-        float2* pml = reinterpret_cast<float2*>(a.part_ml);
-        constexpr int64_t kUnit = (kDC / 4) * kHc;
-        const auto unit_of = [&](int s2) { return ((int64_t)t * a.splits + s2) * 2 + rank; };
-#pragma unroll 1
-        for (int cc = 0; cc < 8; ++cc) {
-          float o[32];
-          load_o32(tmem + lane_off + kColO + 32 * cc, empty, o);
+        load_o32(o_lane + col, empty, o);
+        if (kSplits > 1) {
+          float acc[32];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            po[unit_of(sp) * kUnit + (64 * half + 8 * cc + i) * kHc + hl] =
-                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        }
-        if (half == 0) pml[unit_of(sp) * kHc + hl] = make_float2(m_used, lt);
-        named_bar_sync(1, 128);
-        if (l == 0) {
-          __threadfence();
-          unsigned long long* slot = &a.part_cnt[(int64_t)t * 2 + rank];
-          const bool last = take_ticket(slot, a.launch_id, a.status) == (uint32_t)a.splits;
-          if (last) *slot = (unsigned long long)a.launch_id << 32;   // a replay counts from zero again
-          S.last_flag = last;
-          __threadfence();
-        }
-        named_bar_sync(1, 128);
-        write_out = S.last_flag != 0;
-        if (write_out) {
-          if (l == 0 && a.status != nullptr) atomicOr(&a.status->ran, DSA_KERNEL_MLA_COMBINE);
-          float w[kMaxSplits];
-          float M = -INFINITY, L = 0.f;
+          for (int i = 0; i < 32; ++i) acc[i] = 0.f;
 #pragma unroll
-          for (int s2 = 0; s2 < kMaxSplits; ++s2) {
-            w[s2] = s2 < a.splits ? __ldcg(&pml[unit_of(s2) * kHc + hl]).x : -INFINITY;
-            M = fmaxf(M, w[s2]);
-          }
+          for (int s2 = 0; s2 < kSplits; ++s2) {
+            if (s2 == sp) {
 #pragma unroll
-          for (int s2 = 0; s2 < kMaxSplits; ++s2) {
-            w[s2] = w[s2] == -INFINITY ? 0.f : exp2f(w[s2] - M);
-            if (s2 < a.splits) L += w[s2] * __ldcg(&pml[unit_of(s2) * kHc + hl]).y;
-          }
-          const float inv = L > 0.f ? 1.f / L : 0.f;
-#pragma unroll 1
-          for (int cc = 0; cc < 8; ++cc) {
-            float acc[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-#pragma unroll
-            for (int s2 = 0; s2 < kMaxSplits; ++s2) {
-              if (s2 >= a.splits) continue;
-              const float4* src = po + unit_of(s2) * kUnit + (64 * half + 8 * cc) * kHc + hl;
+              for (int i = 0; i < 32; ++i) acc[i] = fmaf(w[s2], o[i], acc[i]);
+            } else {
+              const int slot = s2 < sp ? s2 : s2 - 1;
+              const float4* src = reinterpret_cast<const float4*>(smraw + (size_t)slot * kCols * 512) +
+                                  (kMine * cw + 32 * cc) / 4 * 128 + l;
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                const float4 v = __ldcg(src + i * kHc);
+                const float4 v = src[i * 128];
                 acc[4 * i] = fmaf(w[s2], v.x, acc[4 * i]);
                 acc[4 * i + 1] = fmaf(w[s2], v.y, acc[4 * i + 1]);
                 acc[4 * i + 2] = fmaf(w[s2], v.z, acc[4 * i + 2]);
                 acc[4 * i + 3] = fmaf(w[s2], v.w, acc[4 * i + 3]);
               }
             }
-            stage(acc, cc, inv);
           }
-          if (a.lse && half == 0 && head < a.n_heads)
-            a.lse[(int64_t)t * a.n_heads + head] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = acc[i];
         }
       }
-      if (write_out) {
-        named_bar_sync(1, 128);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint4*>(stg + hl * 1024 + (((32 * half + col / 8 + q) ^ (hl & 31)) << 4)) = pack8(&o[8 * q], inv);
+    }
+    const int head = kHc * (int)rank + hl;
+    if (a.lse && sp == 0 && cw == 0 && half == 0 && head < a.n_heads)
+      a.lse[(int64_t)t * a.n_heads + head] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    named_bar_sync(1, kSmThreads);
+    // this pair's pieces of each head: kCols / 8 from each half of the dims
+    const int heads_here = max(0, min(kHc, a.n_heads - kHc * (int)rank));
+    uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + ((int64_t)t * a.n_heads + kHc * (int)rank) * kDC);
+    constexpr int kSeg = kCols / 8;
 #pragma unroll 4
-        for (int i = l; i < heads_here * 64; i += 128) {
-          const int h = i >> 6, ch = i & 63;
-          reinterpret_cast<uint4*>(out)[i] = *reinterpret_cast<const uint4*>(stg + h * 1024 + ((ch ^ (h & 31)) << 4));
-        }
-      }
+    for (int i = threadIdx.x; i < heads_here * 2 * kSeg; i += kSmThreads) {
+      const int h = i / (2 * kSeg), r = i % (2 * kSeg), ch = (r / kSeg) * 32 + sp * kSeg + r % kSeg;
+      out[h * 64 + ch] = *reinterpret_cast<const uint4*>(stg + h * 1024 + ((ch ^ (h & 31)) << 4));
     }
   }
   tc_fence_before();
@@ -537,6 +690,43 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(MlaArgs a, int
   }
 }
 
+using Kernel = void (*)(MlaArgs);
+template <int kSplits>
+constexpr Kernel kernel_of = mla_int4_tc_kernel<kSplits>;
+
+cudaLaunchConfig_t launch_config(cudaLaunchAttribute (&at)[2], int splits, int rows) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * splits * 2));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sizeof(Smem);
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)(splits * 2);
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Clusters of `splits` pairs that can be resident at once on this device (0 if the
+// query fails), looked up once per device.
+int resident_clusters(Kernel kernel, int splits) {
+  static std::atomic<int> cached[kMaxPairs + 1][kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  const int have = cached[splits][dev].load();
+  if (have > 0) return have - 1;
+  cudaLaunchAttribute at[2];
+  cudaLaunchConfig_t cfg = launch_config(at, splits, 1);
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    n = 0;
+  }
+  cached[splits][dev].store(n + 1);
+  return n;
+}
+
 }  // namespace
 
 bool mla_int4_tc_supported(const MlaArgs& a) {
@@ -545,27 +735,30 @@ bool mla_int4_tc_supported(const MlaArgs& a) {
 
 dsa_status launch_mla_int4_tc(const MlaArgs& a, cudaStream_t stream) {
   if (a.num_rows == 0) return DSA_OK;
-  const size_t smem = sizeof(Smem) + 1024;
-  static std::atomic<bool> attr[kMaxDevices] = {};
-  if (dsa_status st = set_smem_limit_once(reinterpret_cast<const void*>(mla_int4_tc_kernel), smem, attr)) return st;
-  const int keys_per_split = (int)(ceil_div64(ceil_div64(a.topk, a.splits), kBlk) * kBlk);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.num_rows * a.splits * 2));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
+  static std::atomic<bool> attr1[kMaxDevices] = {}, attr2[kMaxDevices] = {}, attr4[kMaxDevices] = {};
+  dsa_status st;
+  if ((st = set_smem_limit_once(reinterpret_cast<const void*>(kernel_of<1>), sizeof(Smem), attr1)) ||
+      (st = set_smem_limit_once(reinterpret_cast<const void*>(kernel_of<2>), sizeof(Smem), attr2)) ||
+      (st = set_smem_limit_once(reinterpret_cast<const void*>(kernel_of<4>), sizeof(Smem), attr4)))
+    return st;
+  // key splits: the most whose clusters are all resident at once (a second wave costs
+  // more than a split saves), where the selection has a block of keys for each
+  int splits = 1;
+  Kernel kernel = kernel_of<1>;
+  if (a.topk > 2 * kBlk && a.num_rows <= resident_clusters(kernel_of<4>, 4)) {
+    splits = 4;
+    kernel = kernel_of<4>;
+  } else if (a.topk > kBlk && a.num_rows <= resident_clusters(kernel_of<2>, 2)) {
+    splits = 2;
+    kernel = kernel_of<2>;
+  }
   cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 2;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = launch_config(at, splits, a.num_rows);
+  cfg.stream = stream;
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
   cfg.numAttrs = 2;
-  MlaArgs la = a;
-  la.launch_id = next_launch_id();
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, mla_int4_tc_kernel, la, keys_per_split);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
   if (e != cudaSuccess) {
     set_error("mla_int4_tc launch: %s", cudaGetErrorString(e));
     return DSA_ERR_CUDA;

@@ -159,11 +159,6 @@ __device__ __forceinline__ void stage_bf16(uint8_t* stg, int h, int c0, const fl
   for (int q = 0; q < 4; ++q)
     *reinterpret_cast<uint4*>(stg + h * 512 + (((c0 + q) ^ (h & 31)) << 4)) = pack8(&o[8 * q], inv);
 }
-__device__ __forceinline__ void tstamp(long long* tr, uint32_t rank, int ev, int j) {
-  if (tr != nullptr && blockIdx.x < 2 && j < kTraceBlocks)
-    tr[((int)rank * kTraceEvents + ev) * kTraceBlocks + j] = clock64();
-}
-
 __device__ __forceinline__ void setmaxnreg_inc_high() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
 }

@@ -59,12 +59,16 @@ __device__ __forceinline__ ScalePair scale_pair(uint32_t b) {
   p.off = __hmul2(p.s, as_bf162(0xC308C308u));
   return p;
 }
-// Eight dims of one word as four bf16x2, in order.
+// Eight dims of one word as four bf16x2, in order.  (The and-xor is written as one
+// lop3 with both constants in registers: with literals it became two.)
 __device__ __forceinline__ uint4 decode_word(uint32_t w, const ScalePair& p) {
   uint32_t r[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    r[i] = as_u32(__hfma2(as_bf162(((w >> (4 * i)) & 0x000F000Fu) ^ 0x43084308u), p.s, p.off));
+  for (int i = 0; i < 4; ++i) {
+    uint32_t x;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(x) : "r"(w >> (4 * i)), "r"(0x000F000Fu), "r"(0x43084308u));   // (a & b) ^ c
+    r[i] = as_u32(__hfma2(as_bf162(x), p.s, p.off));
+  }
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 

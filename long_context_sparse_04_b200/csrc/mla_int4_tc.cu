@@ -33,8 +33,7 @@
 //                registers one block ahead, then 16-byte stores, swizzled
 //   warps 16-23  decode the values' tile, the same way
 //   warp 24      tensor memory; in the pair's first CTA one thread issues the MMAs
-//   warp 25      resolves the selection to cache rows, two blocks ahead of the
-//                decoding, and prefetches the rows into L2
+//   warp 25      resolves the selection to cache rows, two blocks ahead
 // Tiles, weights and logits have two stages each; S of block j+1 is issued before
 // P V of block j, so that the tensor cores work while the softmax of block j runs.
 //
@@ -75,7 +74,7 @@ struct Smem {                                   // 1024-byte aligned
   uint64_t q_full, k_full[2], v_full[2], p_full[2], s_free[2];
   // arrivals of finished products, in both CTAs
   uint64_t s_full[2], pv_done[2];
-  uint64_t rows_full[2], rows_free[2];
+  uint64_t rows_full[2], rows_free[2], red_full[2];
   uint64_t drained;
   uint32_t tmem_base;
 };
@@ -126,8 +125,25 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint16_t mask) {
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)), "h"(mask) : "memory");
 }
+// Bounded wait; on time-out records DSA_ERR_TIMEOUT (detail = site) and returns
+// false.  Written out so that a barrier already complete costs two instructions:
+// every warp passes two to four of them a block.
 __device__ __forceinline__ bool wait_local(uint64_t* bar, uint32_t parity, DeviceStatus* st, int site) {
-  return mbar_wait(bar, parity, st, site, kWaitPolls);
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, %3;\n"
+      "WAIT_%=:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE_%=;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra WAIT_%=;\n"
+      "DONE_%=:\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "n"(kWaitPolls) : "memory");
+  if (!ok) set_status(st, DSA_ERR_TIMEOUT, site);
+  return ok != 0;
 }
 // The same, agreed on by the warp (its lanes go on or leave together).
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, DeviceStatus* st, int site) {
@@ -140,13 +156,15 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Device
 // itself is ordered at CTA scope.  A release at cluster scope would also wait for
 // this thread's global loads in flight: it cost 1,000 cycles an arrive, and a
 // block 5,800 cycles instead of 2,700.
+// `first`: this CTA's shared-memory window mapped to the pair's first CTA, minus the
+// local window (mapa of the base, taken once).
 __device__ __forceinline__ void warp_arrive_first(uint64_t* bar, uint32_t first) {
   __syncwarp();
-  if ((threadIdx.x & 31) == 0)
-    asm volatile(
-        "{\n\t.reg .b32 ra;\n\t"
-        "mapa.shared::cluster.u32 ra, %0, %1;\n\t"
-        "mbarrier.arrive.release.cta.shared::cluster.b64 _, [ra];\n\t}" ::"r"(smem_u32(bar)), "r"(first) : "memory");
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .u32 l;\n\t"
+      "mov.u32 l, %%laneid;\n\t"
+      "setp.eq.u32 p, l, 0;\n\t"
+      "@p mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar) + first) : "memory");
 }
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
@@ -207,11 +225,10 @@ __device__ __forceinline__ void issue_products(Smem& S, const MlaArgs& a, uint32
 // loads of a block's block-table entries and of the next block's positions are in
 // flight while the block before is handed over.
 __device__ __forceinline__ void resolve_rows(Smem& S, const MlaArgs& a, int t, int seq, int klen, int k0, int nvalid,
-                                             int nblk, uint32_t rank) {
+                                             int nblk) {
   const int lane = threadIdx.x & 31;
   const int32_t* idx = a.idx + (int64_t)t * a.topk + k0;
   const CacheMap& m = a.map;
-  const uint8_t* latent = static_cast<const uint8_t*>(a.latent);
   const int32_t* table = m.block_table ? m.block_table + (int64_t)seq * m.max_pages_per_seq : nullptr;
   const int64_t start = !m.block_table && m.seq_start ? (int64_t)__ldg(m.seq_start + seq) : 0;
   const auto position = [&](int j, int u) {
@@ -276,11 +293,6 @@ __device__ __forceinline__ void resolve_rows(Smem& S, const MlaArgs& a, int t, i
       e0[u] = e1[u];
     }
     warp_arrive(&S.rows_full[j & 1]);
-    // each CTA of the pair prefetches half of the block's rows
-    const int mine = rank ? row[1] : row[0];
-    if (mine >= 0)
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(latent + (int64_t)mine * kRow.bytes), "n"(kRow.bytes)
-                   : "memory");
   }
 }
 
@@ -387,16 +399,58 @@ __device__ __forceinline__ void load_o32(uint32_t taddr, bool empty, float (&o)[
   tmem_wait_ld();
 }
 
+// Two fp32 in one 64-bit register pair: one instruction for both.
+__device__ __forceinline__ uint64_t pair_f32(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split_f32(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Softmax state of a thread: lane l of tensor memory (head l % 64, key half l / 64),
 // columns [16 cw, 16 cw + 16) of the lane's 32.
 struct Softmax {
   float m = -INFINITY, sum = 0.f;                 // running maximum (log2 domain) and this thread's sum
   bool dead = false;                              // a wait ran out
 
-  // One block; false when the warpgroups leave together because a wait ran out (a
-  // dead thread goes on to the next block's barrier, so that every barrier and
-  // collective access stays uniform).
-  __device__ __forceinline__ bool block(Smem& S, const MlaArgs& a, uint32_t tmem_lane, int j, float c, uint32_t rank,
+  // The weights of 16 logits as bf16 pairs, their sum in fp32.  While no key of the
+  // head has been visible m counts as 0.
+  __device__ __forceinline__ float weights(const float (&s)[16], float c, uint32_t (&p2)[8]) const {
+    const float mu = (m == -INFINITY) ? 0.f : -m;
+    const uint64_t c2 = pair_f32(c, c), mu2 = pair_f32(mu, mu);
+    uint64_t ls = 0;                              // two running sums
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float z0, z1;
+      split_f32(fma_f32x2(pair_f32(s[2 * i], s[2 * i + 1]), c2, mu2), z0, z1);
+      const float p0 = ex2_approx(z0), p1 = ex2_approx(z1);
+      ls = add_f32x2(ls, pair_f32(p0, p1));
+      p2[i] = pack_bf16x2(p0, p1);
+    }
+    float l0, l1;
+    split_f32(ls, l0, l1);
+    return l0 + l1;
+  }
+  // One block.  A thread whose wait ran out (dead) skips its waits and goes on, so
+  // that every arrival and collective access stays uniform.
+  __device__ __forceinline__ void block(Smem& S, const MlaArgs& a, uint32_t tmem_lane, int j, float c, uint32_t rank,
                                         uint32_t first) {
     const int b = j & 1, l = threadIdx.x & 127, cw = threadIdx.x >> 7, half = l >> 6, hl = l & 63;
     dead = dead || !wait_local(&S.s_full[b], (j >> 1) & 1, a.status, 49);
@@ -414,14 +468,19 @@ struct Softmax {
       for (int i = 0; i < 16; ++i)
         if (!((mask >> i) & 1u)) s[i] = -INFINITY;
     }
-    float pm[4];
+    float pm[5];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) pm[i & 3] = (i < 4) ? s[i] : fmaxf(pm[i & 3], s[i]);
-    const float mh = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
+    for (int i = 0; i < 5; ++i) pm[i] = max3(s[3 * i], s[3 * i + 1], s[3 * i + 2]);
+    const float mh = fmaxf(max3(pm[0], pm[1], pm[2]), max3(pm[3], pm[4], s[15]));
     S.red[b][cw][l] = mh;
-    if (named_bar_or(1, kSmThreads, dead)) { dead = true; return false; }
+    warp_arrive(&S.red_full[b]);
+    // p = 2^(c s - m) with the running maximum so far, while the other threads'
+    // maxima arrive: it rarely moves
+    uint32_t p2[8];
+    float ls = weights(s, c, p2);
+    dead = dead || !wait_local(&S.red_full[b], (j >> 1) & 1, a.status, 55);
     // the four threads of a head take the same maximum
-    const float mb = c * fmaxf(fmaxf(mh, S.red[b][cw][l ^ 64]), fmaxf(S.red[b][cw ^ 1][l], S.red[b][cw ^ 1][l ^ 64]));
+    const float mb = c * fmaxf(mh, max3(S.red[b][cw][l ^ 64], S.red[b][cw ^ 1][l], S.red[b][cw ^ 1][l ^ 64]));
     // lazy rescale: P stays <= 2^8.  Warp-uniform (tensor-memory access is collective)
     const bool need = mb > m + kRescale;
     if (__any_sync(0xffffffffu, need)) {
@@ -444,20 +503,9 @@ struct Softmax {
       }
       sum *= alpha;
       m = m_new;
+      ls = weights(s, c, p2);
     }
-    // p = 2^(c s - m); while no key of the head has been visible m counts as 0
-    const float mu = (m == -INFINITY) ? 0.f : -m;
-    uint32_t p2[8];
-    float ls[2] = {0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float p0 = ex2_approx(fmaf(s[2 * i], c, mu));
-      const float p1 = ex2_approx(fmaf(s[2 * i + 1], c, mu));
-      ls[0] += p0;
-      ls[1] += p1;
-      p2[i] = pack_bf16x2(p0, p1);
-    }
-    sum += ls[0] + ls[1];
+    sum += ls;
     // the weights' tile is free once P V of block j-2 is done
     dead = dead || !wait_local(&S.pv_done[b], ((j >> 1) & 1) ^ 1, a.status, 51);
     uint8_t* p = S.p[b];
@@ -467,7 +515,6 @@ struct Softmax {
     tc_fence_before();
     warp_arrive_first(&S.p_full[b], first);
     if (threadIdx.x == 0) tstamp(a.trace, rank, 6, j);
-    return true;
   }
 };
 
@@ -479,6 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(MlaArgs a) {
   const int warp = threadIdx.x >> 5;
   const uint32_t crank = cluster_ctarank(), rank = crank & 1u, first = crank & ~1u;
   const int sp = (int)(crank >> 1);
+  const uint32_t to_first = mapa(smraw, first) - smem_u32(smraw);
   const int t = blockIdx.x / (2 * kSplits);
   pdl_launch_dependents();
 
@@ -494,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(MlaArgs a) {
       mbar_init(&S.s_full[i], 1);
       mbar_init(&S.pv_done[i], 1);
       mbar_init(&S.rows_full[i], 1);
+      mbar_init(&S.red_full[i], kSmWarps);
       mbar_init(&S.rows_free[i], 2 * kDecWarps);
     }
     fence_mbar_init();
@@ -524,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(MlaArgs a) {
     if (rank == 0 && !empty && elect_one()) issue_products(S, a, tmem, nblk, (uint16_t)(3u << first));
     __syncwarp();
   } else if (warp == kRowWarp) {
-    if (!empty) resolve_rows(S, a, t, seq, klen, k0, nvalid, nblk, rank);
+    if (!empty) resolve_rows(S, a, t, seq, klen, k0, nvalid, nblk);
   } else if (warp >= kKWarp0) {
     if (!empty) {
       // Q lands while the selection is resolved; heads beyond H are zeros
@@ -536,14 +585,13 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(MlaArgs a) {
         const bool in = h0 + h < a.n_heads;
         cp_async_16_zfill(S.q[c >> 3] + sw128_off(h, c & 7), q + (int64_t)(in ? h0 + h : 0) * kD + 8 * c, in);
       }
-      if (warp >= kVWarp0) decode_blocks<true>(S, a, nblk, rank, first, warp - kVWarp0);
-      else decode_blocks<false>(S, a, nblk, rank, first, warp - kKWarp0);
+      if (warp >= kVWarp0) decode_blocks<true>(S, a, nblk, rank, to_first, warp - kVWarp0);
+      else decode_blocks<false>(S, a, nblk, rank, to_first, warp - kKWarp0);
     }
   } else {
     const float c = a.sm_scale * kLog2e;
     const uint32_t tmem_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    for (int j = 0; j < nblk; ++j)
-      if (!sm.block(S, a, tmem_lane, j, c, rank, first)) break;
+    for (int j = 0; j < nblk; ++j) sm.block(S, a, tmem_lane, j, c, rank, to_first);
     if (!sm.dead && !empty) {
       sm.dead = !wait_local(&S.pv_done[(nblk - 1) & 1], ((nblk - 1) >> 1) & 1, a.status, 52);
       tc_fence_after();

@@ -156,6 +156,10 @@ __device__ __forceinline__ void bulk_wait_read0() {
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
+// Arrives without waiting (the others sync on the same barrier and count).
+__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t nthreads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
 // Named barrier that also returns the OR of `v` over the participating threads.
 __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t nthreads, bool v) {
   uint32_t r;

@@ -26,14 +26,18 @@
 // values that is cheaper than an exchange through distributed shared memory.
 //
 // Roles per CTA (832 threads):
-//   warps 0-7    softmax and output: two threads per TMEM lane, 16 keys of a head
-//                each; a head's four threads share its maximum through shared
-//                memory.  Lazy rescale as in mla_tc.cu.
+//   warps 0-7    softmax and output, two groups of four warps that take the blocks in
+//                turn: a block's chain (wait, tensor-memory load, maximum, weights,
+//                store) is longer than its products take, so one group would set the
+//                pace.  Thread = TMEM lane, 32 keys of a head; the head's other 32 are
+//                lane + 64.  The running maximum passes from group to group through
+//                shared memory (a few hundred cycles a block); each thread keeps its
+//                own sum.  Lazy rescale as in mla_tc.cu.
 //   warps 8-15   decode the keys' tile: packed pieces from global memory to
 //                registers one block ahead, then 16-byte stores, swizzled
 //   warps 16-23  decode the values' tile, the same way
 //   warp 24      tensor memory; in the pair's first CTA one thread issues the MMAs
-//   warp 25      resolves the selection to cache rows, two blocks ahead
+//   warp 25      resolves the selection to cache rows, two blocks at a time
 // Tiles, weights and logits have two stages each; S of block j+1 is issued before
 // P V of block j, so that the tensor cores work while the softmax of block j runs.
 //
@@ -67,25 +71,35 @@ struct Smem {                                   // 1024-byte aligned
   uint8_t k[2][kQChunks][kHalfBlk * 128];       // its 32 keys, 576 dims
   uint8_t v[2][4][kBlk * 128];                  // 64 keys, its 256 dims
   uint8_t p[2][kHc * 128];                      // its heads' weights of 64 keys
-  float red[2][2][2 * kHc];                     // block maxima, [parity][column half][lane]; the final sums
-  int32_t rows[2][kBlk];                        // physical cache row per key of a block, -1 = none
+  float red[2][2 * kHc];                        // by softmax group and lane: block maxima; the final sums
+  float m_run[2][kHc];                          // running maximum of a head after a group's block
+  int32_t rows[2][2 * kBlk];                    // cache row per key of two blocks, -1 = none
   uint32_t valid[kMaxKeys / 32];                // per 32 keys: bit i set = key i has a row
   // waited for by the issuing thread, in the pair's first CTA
-  uint64_t q_full, k_full[2], v_full[2], p_full[2], s_free[2];
+  uint64_t q_full, k_full[2], v_full[2], p_full[2];
   // arrivals of finished products, in both CTAs
   uint64_t s_full[2], pv_done[2];
-  uint64_t rows_full[2], rows_free[2], red_full[2];
+  uint64_t rows_full[2], rows_free[2];
+  uint64_t merged;                              // the other splits' parts have arrived
   uint64_t drained;
   uint32_t tmem_base;
 };
 static_assert(sizeof(Smem) <= 227 * 1024, "shared memory of the attention kernel");
 static_assert(offsetof(Smem, k) % 1024 == 0 && offsetof(Smem, v) % 1024 == 0 && offsetof(Smem, p) % 1024 == 0, "swizzle");
-// The merge of a row's key splits: the split's pair s finishes columns
-// [256 s / S, 256 (s + 1) / S) of every lane and receives them from the other
-// pairs, [source][column / 4][lane] float4, where Q and K lay; then (max, sum) per
-// source and head.
-constexpr size_t kMlOff = 3 * 32768;
-static_assert(kMlOff + kMaxPairs * kHc * sizeof(float2) <= offsetof(Smem, v), "merge layout");
+// The merge of a row's key splits S: pair s finishes columns [256 s / S, 256 (s + 1) / S)
+// of every lane and gets them from the other pairs, [source][column / 4][lane] float4,
+// where Q lay, with (max, sum) per source and head; it sends its other columns from
+// behind that.  Rows of the finished output are staged behind those.
+constexpr size_t kRecvMl = 3 * 32768, kSendMl = kRecvMl + kMaxPairs * kHc * 8, kSend = kRecvMl + 4096;
+template <int kSplits>
+struct Merge {
+  static constexpr int kCols = 256 / kSplits;                   // columns of a lane that a pair finishes
+  static constexpr uint32_t kPart = kCols * 512, kMl = kHc * 8; // bytes of one source's part
+  static constexpr size_t kOut = kSplits == 1 ? offsetof(Smem, v) : kSend + (kSplits - 1) * (size_t)kPart;
+  static constexpr int kOutRow = 4 * kCols + 16;                // bytes of a staged head: odd in 16-byte pieces
+  static_assert((kSplits - 1) * (size_t)kPart <= kRecvMl, "receive area");
+  static_assert(kOut % 128 == 0 && kOut + kHc * (size_t)kOutRow <= offsetof(Smem, red), "send and output areas");
+};
 
 // ---------------------------------------------------------------- two-CTA tcgen05
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* smem_dst, uint32_t ncols) {
@@ -184,8 +198,8 @@ __device__ __forceinline__ void issue_products(Smem& S, const MlaArgs& a, uint32
   for (int j = 0; ok && j <= nblk; ++j) {
     if (j < nblk) {
       const int b = j & 1;
-      ok = wait_local(&S.k_full[b], (j >> 1) & 1, status, 42) && wait_local(&S.s_free[b], ((j >> 1) & 1) ^ 1, status, 43);
-      if (!ok) break;
+      // (S of block j-2 has been read: P V of that block waited for its weights)
+      if (!(ok = wait_local(&S.k_full[b], (j >> 1) & 1, status, 42))) break;
       tc_fence_after();
       const uint64_t kd = kd0 + (uint64_t)(b * (sizeof(S.k[0]) >> 4));
       const uint32_t d = tmem + kColS + b * 32;
@@ -221,32 +235,35 @@ __device__ __forceinline__ void issue_products(Smem& S, const MlaArgs& a, uint32
 }
 
 // ---------------------------------------------------------------- the selection
-// One warp turns the selection into cache rows, two keys of a block per lane: the
-// loads of a block's block-table entries and of the next block's positions are in
-// flight while the block before is handed over.
+// One warp turns the selection into cache rows, two blocks (four keys a lane) at a
+// time: their block-table entries and the next positions are in flight while the
+// two before are handed over.
 __device__ __forceinline__ void resolve_rows(Smem& S, const MlaArgs& a, int t, int seq, int klen, int k0, int nvalid,
                                              int nblk) {
+  constexpr int kKeys = 2 * kBlk / 32;
   const int lane = threadIdx.x & 31;
   const int32_t* idx = a.idx + (int64_t)t * a.topk + k0;
   const CacheMap& m = a.map;
   const int32_t* table = m.block_table ? m.block_table + (int64_t)seq * m.max_pages_per_seq : nullptr;
   const int64_t start = !m.block_table && m.seq_start ? (int64_t)__ldg(m.seq_start + seq) : 0;
-  const auto position = [&](int j, int u) {
-    const int i = j * kBlk + 32 * u + lane;
-    const int s = i < nvalid ? __ldg(idx + i) : -1;
-    return s < klen ? s : -1;
+  const auto positions = [&](int p, int (&s)[kKeys]) {
+#pragma unroll
+    for (int u = 0; u < kKeys; ++u) {
+      const int i = p * 2 * kBlk + 32 * u + lane;
+      s[u] = i < nvalid ? __ldg(idx + i) : -1;
+      if (s[u] >= klen) s[u] = -1;
+    }
   };
   const auto page_of = [&](int s) { return m.page_shift >= 0 ? s >> m.page_shift : s / m.page_size; };
-  // the block-table entry of position s (-1: none)
-  const auto entry = [&](int s) {
-    if (s < 0 || table == nullptr) return -1;
-    const int pg = page_of(s);
-    if (pg >= m.max_pages_per_seq) {
-      set_status(a.status, DSA_ERR_OUT_OF_RANGE, s);
-      return -1;
+  const auto entries = [&](const int (&s)[kKeys], int (&e)[kKeys]) {
+#pragma unroll
+    for (int u = 0; u < kKeys; ++u) {
+      e[u] = -1;
+      if (s[u] < 0 || table == nullptr) continue;
+      const int pg = page_of(s[u]);
+      if (pg < m.max_pages_per_seq) e[u] = __ldg(table + pg);
+      else set_status(a.status, DSA_ERR_OUT_OF_RANGE, s[u]);
     }
-    const int p = __ldg(table + pg);
-    return p;
   };
   const auto row_of = [&](int s, int e) {
     if (s < 0) return -1;
@@ -266,33 +283,26 @@ __device__ __forceinline__ void resolve_rows(Smem& S, const MlaArgs& a, int t, i
     }
     return (int)r;
   };
-  int s0[2], s1[2], e0[2];
+  int s0[kKeys], s1[kKeys], s2[kKeys], e0[kKeys], e1[kKeys];
+  positions(0, s0);
+  positions(1, s1);
+  entries(s0, e0);
+  cluster_wait();
+  for (int p = 0; 2 * p < nblk; ++p) {
+    positions(p + 2, s2);
+    entries(s1, e1);
+    if (!wait_warp(&S.rows_free[p & 1], ((p >> 1) & 1) ^ 1, a.status, 53)) break;
 #pragma unroll
-  for (int u = 0; u < 2; ++u) s0[u] = position(0, u);
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    s1[u] = position(1, u);
-    e0[u] = entry(s0[u]);
-  }
-  for (int j = 0; j < nblk; ++j) {
-    int s2[2], e1[2], row[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      s2[u] = position(j + 2, u);
-      e1[u] = entry(s1[u]);
-    }
-    if (!wait_warp(&S.rows_free[j & 1], ((j >> 1) & 1) ^ 1, a.status, 53)) break;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      row[u] = row_of(s0[u], e0[u]);
-      S.rows[j & 1][32 * u + lane] = row[u];
-      const uint32_t bits = __ballot_sync(0xffffffffu, row[u] >= 0);
-      if (lane == 0) S.valid[2 * j + u] = bits;
+    for (int u = 0; u < kKeys; ++u) {
+      const int row = row_of(s0[u], e0[u]);
+      S.rows[p & 1][32 * u + lane] = row;
+      const uint32_t bits = __ballot_sync(0xffffffffu, row >= 0);
+      if (lane == 0) S.valid[kKeys * p + u] = bits;
       s0[u] = s1[u];
       s1[u] = s2[u];
       e0[u] = e1[u];
     }
-    warp_arrive(&S.rows_full[j & 1]);
+    warp_arrive(&S.rows_full[p & 1]);
   }
 }
 
@@ -327,10 +337,9 @@ struct Decoder {
     rope_src = kRow.rope + 16 * (kt & 7);
     rope_dst = 8 * kChunk + sw128_off(kt >> 3, kt & 7);
   }
-  // Loads a block's packed pieces (zeros for a key without a row).
-  __device__ __forceinline__ void load(Pieces& x, const int32_t* rows, const uint8_t* latent) const {
-    const int row = rows[key];
-    const int rrow = kV ? -1 : rows[rope_key];
+  // Loads a block's packed pieces of cache rows `row` (codes) and `rrow` (RoPE key);
+  // zeros for a key without a row.
+  __device__ __forceinline__ void load(Pieces& x, int row, int rrow, const uint8_t* latent) const {
     x.codes[0] = x.codes[1] = x.rope = make_uint4(0u, 0u, 0u, 0u);
     x.scales[0] = x.scales[1] = 0u;
     if (row >= 0) {
@@ -361,20 +370,20 @@ __device__ __forceinline__ void decode_blocks(Smem& S, const MlaArgs& a, int nbl
   const uint8_t* latent = static_cast<const uint8_t*>(a.latent);
   const Decoder<kV> dec(wt, rank);
   typename Decoder<kV>::Pieces even, odd;         // the packed pieces of even and odd blocks
-  const bool stamp = wt == 0 && (threadIdx.x & 31) == 0;
-  const auto fetch = [&](int j, typename Decoder<kV>::Pieces& x) {
-    if (!wait_warp(&S.rows_full[j & 1], (j >> 1) & 1, a.status, 54)) return false;
-    dec.load(x, S.rows[j & 1], latent);
-    warp_arrive(&S.rows_free[j & 1]);
+  const bool stamp = a.trace != nullptr && wt == 0 && (threadIdx.x & 31) == 0;
+  int row[2] = {-1, -1}, rrow[2] = {-1, -1};      // of the two blocks handed over last
+  const auto take_rows = [&](int p) {
+    if (!wait_warp(&S.rows_full[p & 1], (p >> 1) & 1, a.status, 54)) return false;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      row[u] = S.rows[p & 1][u * kBlk + dec.key];
+      if (!kV) rrow[u] = S.rows[p & 1][u * kBlk + dec.rope_key];
+    }
+    warp_arrive(&S.rows_free[p & 1]);
     return true;
   };
-  bool ok = fetch(0, even);
-  cp_async_wait_all();                            // this thread's pieces of Q
-  fence_proxy_async_smem();
-  warp_arrive_first(&S.q_full, first);
-  const auto block = [&](int j, const typename Decoder<kV>::Pieces& now, typename Decoder<kV>::Pieces& next) {
+  const auto block = [&](int j, const typename Decoder<kV>::Pieces& now) {
     const int b = j & 1;
-    if (j + 1 < nblk && !fetch(j + 1, next)) return false;
     // the stage is free once the products of block j-2 have read it
     if (!wait_warp(kV ? &S.pv_done[b] : &S.s_full[b], ((j >> 1) & 1) ^ 1, a.status, kV ? 48 : 47)) return false;
     if (stamp) tstamp(a.trace, rank, kV ? 7 : 5, j);
@@ -384,8 +393,23 @@ __device__ __forceinline__ void decode_blocks(Smem& S, const MlaArgs& a, int nbl
     if (stamp) tstamp(a.trace, rank, kV ? 1 : 0, j);
     return true;
   };
-  for (int j = 0; ok && j < nblk; j += 2)
-    ok = block(j, even, odd) && (j + 1 >= nblk || block(j + 1, odd, even));
+  bool ok = take_rows(0);
+  dec.load(even, row[0], rrow[0], latent);
+  cp_async_wait_all();                            // this thread's pieces of Q
+  fence_proxy_async_smem();
+  cluster_wait();                                 // the first CTA's barriers are initialised
+  warp_arrive_first(&S.q_full, first);
+  for (int j = 0; ok && j < nblk; j += 2) {
+    if (j + 1 < nblk) dec.load(odd, row[1], rrow[1], latent);
+    ok = block(j, even);
+    if (!ok || j + 1 >= nblk) break;
+    if (j + 2 < nblk) {
+      ok = take_rows((j >> 1) + 1);
+      if (!ok) break;
+      dec.load(even, row[0], rrow[0], latent);
+    }
+    ok = block(j + 1, odd);
+  }
 }
 
 // 32 columns of this thread's lane of O (zeros when no product was issued).
@@ -424,97 +448,103 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// Softmax state of a thread: lane l of tensor memory (head l % 64, key half l / 64),
-// columns [16 cw, 16 cw + 16) of the lane's 32.
+// Softmax state of a thread: lane l of tensor memory (head l % 64, keys 32 (l / 64)..
+// of a block), blocks of its group's parity.
 struct Softmax {
-  float m = -INFINITY, sum = 0.f;                 // running maximum (log2 domain) and this thread's sum
+  float m = -INFINITY, sum = 0.f;                 // maximum (log2 domain) that the sum refers to, sum
   bool dead = false;                              // a wait ran out
 
-  // The weights of 16 logits as bf16 pairs, their sum in fp32.  While no key of the
-  // head has been visible m counts as 0.
-  __device__ __forceinline__ float weights(const float (&s)[16], float c, uint32_t (&p2)[8]) const {
+  // One block of group g = j % 2.  A thread whose wait ran out (dead) skips its waits
+  // and goes on, so that every arrival and collective access stays uniform.
+  __device__ __forceinline__ void block(Smem& S, const MlaArgs& a, uint32_t tmem_lane, int j, int nblk, int g, float c,
+                                        uint32_t rank, uint32_t first) {
+    const int l = threadIdx.x & 127, half = l >> 6, hl = l & 63;
+    const uint32_t phase = (j >> 1) & 1;
+    dead = dead || !wait_local(&S.s_full[g], phase, a.status, 49);
+    tc_fence_after();
+    if (l == 0 && a.trace != nullptr) tstamp(a.trace, rank, 4, j);
+    float s[32];
+    tmem_ld32(tmem_lane + kColS + g * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+    tmem_wait_ld();
+    // masked keys are -inf (a full block needs no test)
+    const uint32_t mask = S.valid[2 * j + half];
+    if (mask != 0xFFFFFFFFu) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (!((mask >> i) & 1u)) s[i] = -INFINITY;
+    }
+    float pm[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pm[i] = max3(s[2 * i], s[2 * i + 1], s[8 + i]);
+#pragma unroll
+    for (int i = 12; i < 32; i += 8)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) pm[k] = i + 4 + k < 32 ? max3(pm[k], s[i + k], s[i + 4 + k]) : fmaxf(pm[k], s[i + k]);
+    const float mh = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
+    S.red[g][l] = mh;
+    // named barriers, not mbarriers: even a wait that is already met costs ~200 cycles
+    // on an mbarrier, and this chain sets the pace.  First the running maximum after
+    // the other group's block j-1, then this block's from the group's other warps.
+    if (j > 0) named_bar_sync(4 + (g ^ 1), kSmThreads);
+    float m_now = j > 0 ? S.m_run[g ^ 1][hl] : -INFINITY;
+    named_bar_sync(2 + g, kSmThreads / 2);
+    const float mb = c * fmaxf(mh, S.red[g][l ^ 64]);
+    // lazy rescale: P stays <= 2^8.  Warp-uniform (tensor-memory access is collective);
+    // the two lanes of a head decide alike
+    const bool need = mb > m_now + kRescale;
+    if (__any_sync(0xffffffffu, need)) {
+      const float m_new = need ? mb : m_now;
+      const float alpha = need ? (m_now == -INFINITY ? 0.f : exp2f(m_now - m_new)) : 1.f;
+      if (j > 0) {
+        // no product is in flight: block j-1's is done, block j's waits for P below
+        dead = dead || !wait_local(&S.pv_done[g ^ 1], ((j - 1) >> 1) & 1, a.status, 50);
+        tc_fence_after();
+#pragma unroll 1
+        for (int cc = 0; cc < 16; ++cc) {
+          uint32_t o[16];
+          const uint32_t col = tmem_lane + kColO + 16 * cc;
+          tmem_ld16(col, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          tmem_st16(col, o);
+        }
+        tmem_wait_st();
+      }
+      m_now = m_new;
+    }
+    if (half == 0) S.m_run[g][hl] = m_now;
+    if (j + 1 < nblk) named_bar_arrive(4 + g, kSmThreads);
+    if (__any_sync(0xffffffffu, m != m_now)) {
+      sum *= m == -INFINITY ? 0.f : exp2f(m - m_now);
+      m = m_now;
+    }
+    // (the weights' tile is free: P V of block j-2 was issued before S of this block,
+    // and a commit covers all that was issued before it)
+    // p = 2^(c s - m); while no key of the head has been visible m counts as 0
     const float mu = (m == -INFINITY) ? 0.f : -m;
     const uint64_t c2 = pair_f32(c, c), mu2 = pair_f32(mu, mu);
     uint64_t ls = 0;                              // two running sums
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float z0, z1;
-      split_f32(fma_f32x2(pair_f32(s[2 * i], s[2 * i + 1]), c2, mu2), z0, z1);
-      const float p0 = ex2_approx(z0), p1 = ex2_approx(z1);
-      ls = add_f32x2(ls, pair_f32(p0, p1));
-      p2[i] = pack_bf16x2(p0, p1);
-    }
-    float l0, l1;
-    split_f32(ls, l0, l1);
-    return l0 + l1;
-  }
-  // One block.  A thread whose wait ran out (dead) skips its waits and goes on, so
-  // that every arrival and collective access stays uniform.
-  __device__ __forceinline__ void block(Smem& S, const MlaArgs& a, uint32_t tmem_lane, int j, float c, uint32_t rank,
-                                        uint32_t first) {
-    const int b = j & 1, l = threadIdx.x & 127, cw = threadIdx.x >> 7, half = l >> 6, hl = l & 63;
-    dead = dead || !wait_local(&S.s_full[b], (j >> 1) & 1, a.status, 49);
-    tc_fence_after();
-    if (threadIdx.x == 0) tstamp(a.trace, rank, 4, j);
-    float s[16];
-    tmem_ld16(tmem_lane + kColS + b * 32 + 16 * cw, *reinterpret_cast<uint32_t(*)[16]>(&s[0]));
-    tmem_wait_ld();
-    tc_fence_before();
-    warp_arrive_first(&S.s_free[b], first);
-    // masked keys are -inf (whole words of a full block need no test)
-    const uint32_t mask = S.valid[2 * j + half] >> (16 * cw);
-    if ((mask & 0xFFFFu) != 0xFFFFu) {
+    for (int q = 0; q < 4; ++q) {
+      uint32_t p2[4];
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (!((mask >> i) & 1u)) s[i] = -INFINITY;
-    }
-    float pm[5];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) pm[i] = max3(s[3 * i], s[3 * i + 1], s[3 * i + 2]);
-    const float mh = fmaxf(max3(pm[0], pm[1], pm[2]), max3(pm[3], pm[4], s[15]));
-    S.red[b][cw][l] = mh;
-    warp_arrive(&S.red_full[b]);
-    // p = 2^(c s - m) with the running maximum so far, while the other threads'
-    // maxima arrive: it rarely moves
-    uint32_t p2[8];
-    float ls = weights(s, c, p2);
-    dead = dead || !wait_local(&S.red_full[b], (j >> 1) & 1, a.status, 55);
-    // the four threads of a head take the same maximum
-    const float mb = c * fmaxf(mh, max3(S.red[b][cw][l ^ 64], S.red[b][cw ^ 1][l], S.red[b][cw ^ 1][l ^ 64]));
-    // lazy rescale: P stays <= 2^8.  Warp-uniform (tensor-memory access is collective)
-    const bool need = mb > m + kRescale;
-    if (__any_sync(0xffffffffu, need)) {
-      const float m_new = need ? mb : m;
-      const float alpha = need ? (m == -INFINITY ? 0.f : exp2f(m - m_new)) : 1.f;
-      if (j > 0) {
-        dead = dead || !wait_local(&S.pv_done[b ^ 1], ((j - 1) >> 1) & 1, a.status, 50);
-        tc_fence_after();
-#pragma unroll 1
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t o[32];
-          const uint32_t col = tmem_lane + kColO + 128 * cw + 32 * cc;
-          tmem_ld32(col, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-          tmem_st32(col, o);
-        }
-        tmem_wait_st();
+      for (int i = 0; i < 4; ++i) {
+        float z0, z1;
+        split_f32(fma_f32x2(pair_f32(s[8 * q + 2 * i], s[8 * q + 2 * i + 1]), c2, mu2), z0, z1);
+        const float p0 = ex2_approx(z0), p1 = ex2_approx(z1);
+        ls = add_f32x2(ls, pair_f32(p0, p1));
+        p2[i] = pack_bf16x2(p0, p1);
       }
-      sum *= alpha;
-      m = m_new;
-      ls = weights(s, c, p2);
+      *reinterpret_cast<uint4*>(S.p[g] + sw128_off(hl, 4 * half + q)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
     }
-    sum += ls;
-    // the weights' tile is free once P V of block j-2 is done
-    dead = dead || !wait_local(&S.pv_done[b], ((j >> 1) & 1) ^ 1, a.status, 51);
-    uint8_t* p = S.p[b];
-    *reinterpret_cast<uint4*>(p + sw128_off(hl, 4 * half + 2 * cw)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
-    *reinterpret_cast<uint4*>(p + sw128_off(hl, 4 * half + 2 * cw + 1)) = make_uint4(p2[4], p2[5], p2[6], p2[7]);
     fence_proxy_async_smem();
     tc_fence_before();
-    warp_arrive_first(&S.p_full[b], first);
-    if (threadIdx.x == 0) tstamp(a.trace, rank, 6, j);
+    warp_arrive_first(&S.p_full[g], first);
+    float l0, l1;
+    split_f32(ls, l0, l1);
+    sum += l0 + l1;
+    if (l == 0 && a.trace != nullptr) tstamp(a.trace, rank, 6, j);
   }
 };
 
@@ -537,22 +567,22 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(MlaArgs a) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.k_full[i], 2 * kDecWarps);
       mbar_init(&S.v_full[i], 2 * kDecWarps);
-      mbar_init(&S.p_full[i], 2 * kSmWarps);
-      mbar_init(&S.s_free[i], 2 * kSmWarps);
+      mbar_init(&S.p_full[i], kSmWarps);         // a group's four warps in each CTA
       mbar_init(&S.s_full[i], 1);
       mbar_init(&S.pv_done[i], 1);
       mbar_init(&S.rows_full[i], 1);
-      mbar_init(&S.red_full[i], kSmWarps);
       mbar_init(&S.rows_free[i], 2 * kDecWarps);
     }
+    mbar_init(&S.merged, 1);
     fence_mbar_init();
+    if (kSplits > 1) mbar_expect_tx(&S.merged, (kSplits - 1) * (Merge<kSplits>::kPart + Merge<kSplits>::kMl));
   }
   __syncwarp();
   if (warp == kMmaWarp) tmem_alloc_pair(&S.tmem_base, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  cluster_sync();                       // the pair's barriers are initialised
+  cluster_arrive();                     // waited for before anything touches another CTA
   const uint32_t tmem = S.tmem_base;
   pdl_wait();
   trace_kernel(a.status, DSA_KERNEL_MLA_INT4_TC);
@@ -570,10 +600,12 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(MlaArgs a) {
   Softmax sm;
 
   if (warp == kMmaWarp) {
+    cluster_wait();
     if (rank == 0 && !empty && elect_one()) issue_products(S, a, tmem, nblk, (uint16_t)(3u << first));
     __syncwarp();
   } else if (warp == kRowWarp) {
     if (!empty) resolve_rows(S, a, t, seq, klen, k0, nvalid, nblk);
+    else cluster_wait();
   } else if (warp >= kKWarp0) {
     if (!empty) {
       // Q lands while the selection is resolved; heads beyond H are zeros
@@ -587,147 +619,139 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(MlaArgs a) {
       }
       if (warp >= kVWarp0) decode_blocks<true>(S, a, nblk, rank, to_first, warp - kVWarp0);
       else decode_blocks<false>(S, a, nblk, rank, to_first, warp - kKWarp0);
+    } else {
+      cluster_wait();
     }
   } else {
+    cluster_wait();
     const float c = a.sm_scale * kLog2e;
     const uint32_t tmem_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    for (int j = 0; j < nblk; ++j) sm.block(S, a, tmem_lane, j, c, rank, to_first);
+    const int g = warp >> 2;
+    for (int j = g; j < nblk; j += 2) sm.block(S, a, tmem_lane, j, nblk, g, c, rank, to_first);
     if (!sm.dead && !empty) {
       sm.dead = !wait_local(&S.pv_done[(nblk - 1) & 1], ((nblk - 1) >> 1) & 1, a.status, 52);
       tc_fence_after();
     }
   }
+
   // The row's output.  With key splits the pairs of the cluster first exchange what
-  // they hold: every pair's products are done at the first barrier, so the tiles
-  // may be overwritten; at the second everything has arrived.
+  // they hold, once every pair's products are done and its tiles may be overwritten.
+  using Mg = Merge<kSplits>;
+  constexpr int kCols = Mg::kCols;
   if (kSplits > 1) {
     tc_fence_before();
     __syncthreads();
     cluster_sync();
     tc_fence_after();
   }
-  const int l = threadIdx.x & 127, cw = threadIdx.x >> 7, half = l >> 6, hl = l & 63;
-  const bool out_warp = warp < kSmWarps;
-  const uint32_t o_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColO;
-  bool fail = false;
-  float lt = 0.f;
-  if (out_warp) {
-    // the head's sum over its four threads; a wait that ran out anywhere fails the CTA
+  if (warp < kSmWarps) {
+    const int l = threadIdx.x & 127, cw = threadIdx.x >> 7, half = l >> 6, hl = l & 63;
+    const uint32_t o_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColO;
+    // the head's maximum and its sum over four threads; a wait that ran out anywhere
+    // fails the CTA
+    const bool fail = named_bar_or(1, kSmThreads, sm.dead);
+    float M = empty ? -INFINITY : S.m_run[(nblk - 1) & 1][hl];
+    S.red[cw][l] = sm.m == -INFINITY ? 0.f : sm.sum * exp2f(sm.m - M);
     named_bar_sync(1, kSmThreads);
-    S.red[0][cw][l] = sm.sum;
-    fail = named_bar_or(1, kSmThreads, sm.dead);
-    lt = (S.red[0][0][hl] + S.red[0][1][hl]) + (S.red[0][0][hl + 64] + S.red[0][1][hl + 64]);
-    if (fail) lt = __int_as_float(0x7FC00000);    // marks the row for the other pairs too
-  }
-  constexpr int kCols = 256 / kSplits;            // columns of each lane that a pair finishes
-  if (kSplits > 1) {
-    if (out_warp) {
+    float L = (S.red[0][hl] + S.red[1][hl]) + (S.red[0][hl + 64] + S.red[1][hl + 64]);
+    if (fail) L = __int_as_float(0x7FC00000);     // marks the row for the other pairs too
+    float w[kSplits];
+    w[0] = 1.f;
+    bool got = true;
+    if (kSplits > 1) {
+      // parts for the other pairs, 32 columns at a time: staged, then one bulk copy
 #pragma unroll 1
-      for (int cc = 0; cc < 4; ++cc) {            // this thread's half of the columns, 32 at a time
+      for (int cc = 0; cc < 4; ++cc) {
         const int col = 128 * cw + 32 * cc, to = col / kCols;
         if (to == sp) continue;
         float o[32];
         load_o32(o_lane + col, empty || fail, o);
-        const uint32_t peer = (uint32_t)(2 * to) + rank;
-        const int slot = sp < to ? sp : sp - 1;   // the receiver's other pairs in order
-        const uint32_t dst = mapa(smraw + (size_t)slot * kCols * 512 + (size_t)((col - to * kCols) / 4 * 128 + l) * 16, peer);
+        const int out_slot = to < sp ? to : to - 1, in_slot = sp < to ? sp : sp - 1;
+        const size_t off = (size_t)(col - to * kCols) * 512;
+        uint8_t* src = smraw + kSend + out_slot * (size_t)Mg::kPart + off;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          st_dsmem_v4(dst + i * 128 * 16, __float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
-                      __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3]));
+          *reinterpret_cast<float4*>(src + (i * 128 + l) * 16) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        fence_proxy_async_smem();
+        named_bar_sync(2 + cw, 128);
+        if (l == 0)
+          bulk_copy_to_peer(smraw + in_slot * (size_t)Mg::kPart + off, src, 32 * 512, &S.merged, (uint32_t)(2 * to) + rank);
       }
-      if (cw == 0 && half == 0) {
-#pragma unroll
-        for (int to = 0; to < kSplits; ++to) {
-          const uint32_t dst = mapa(smraw + kMlOff + (size_t)(sp * kHc + hl) * sizeof(float2), (uint32_t)(2 * to) + rank);
-          st_dsmem_u32(dst, __float_as_uint(sm.m));
-          st_dsmem_u32(dst + 4, __float_as_uint(lt));
-        }
-      }
-    }
-    tc_fence_before();
-    __syncthreads();
-    cluster_sync();
-    tc_fence_after();
-  }
-  if (out_warp) {
-    // out = sum_s w_s O_s / sum_s w_s l_s,  w_s = 2^(m_s - max m), splits in order
-    float w[kSplits], M = sm.m, L = lt;
-    if (kSplits == 1) {
-      w[0] = 1.f;
-    } else {
-      const float2* ml = reinterpret_cast<const float2*>(smraw + kMlOff);
+      float2* ml = reinterpret_cast<float2*>(smraw + kSendMl);
+      if (cw == 0 && half == 0) ml[hl] = make_float2(M, L);
+      fence_proxy_async_smem();
+      named_bar_sync(1, kSmThreads);
+      if (threadIdx.x < kSplits && threadIdx.x != sp)
+        bulk_copy_to_peer(smraw + kRecvMl + sp * (size_t)Mg::kMl, ml, Mg::kMl, &S.merged, 2 * threadIdx.x + rank);
+      bulk_commit();
+      got = wait_local(&S.merged, 0, a.status, 57);
+      // out = sum_s w_s O_s / sum_s w_s l_s,  w_s = 2^(m_s - max m), splits in order
+      const float2 mine = make_float2(M, L);
       M = -INFINITY;
       L = 0.f;
-#pragma unroll
-      for (int s2 = 0; s2 < kSplits; ++s2) M = fmaxf(M, ml[s2 * kHc + hl].x);
+      float2 v[kSplits];
 #pragma unroll
       for (int s2 = 0; s2 < kSplits; ++s2) {
-        const float2 v = ml[s2 * kHc + hl];
-        w[s2] = v.x == -INFINITY ? 0.f : exp2f(v.x - M);
-        L += v.x == -INFINITY ? 0.f * v.y : w[s2] * v.y;      // NaN of a failed pair stays
+        v[s2] = s2 == sp ? mine : reinterpret_cast<const float2*>(smraw + kRecvMl + s2 * (size_t)Mg::kMl)[hl];
+        M = fmaxf(M, v[s2].x);
+      }
+#pragma unroll
+      for (int s2 = 0; s2 < kSplits; ++s2) {
+        w[s2] = v[s2].x == -INFINITY ? 0.f : exp2f(v[s2].x - M);
+        L += w[s2] * v[s2].y;                     // NaN of a failed pair stays
       }
     }
-    const bool bad = L != L;
+    const bool bad = named_bar_or(1, kSmThreads, !got) || L != L;
     const float inv = L > 0.f ? 1.f / L : 0.f;
-    // Finished rows go through shared memory (the values' tiles, idle now) so that
-    // global writes are whole segments: 64 heads x 64 pieces of 16 bytes, piece c of
-    // head h at c ^ (h % 32).
-    uint8_t* stg = S.v[0][0];
+    // Finished rows go through shared memory, so that each head's columns leave as
+    // two bulk copies (one from each half of the dims).
+    uint8_t* stg = smraw + Mg::kOut + (size_t)hl * Mg::kOutRow + half * 2 * kCols;
     constexpr int kMine = kCols / 2;              // columns of this thread: 128, 64 or 32
 #pragma unroll 1
     for (int cc = 0; cc < kMine / 32; ++cc) {
-      const int col = sp * kCols + kMine * cw + 32 * cc;
+      const int col = kMine * cw + 32 * cc;       // within the pair's columns
       float o[32];
-      if (bad) {
+      load_o32(o_lane + sp * kCols + col, empty || bad, o);
+      if (kSplits > 1) {
+        float acc[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = 0.f;
-      } else {
-        load_o32(o_lane + col, empty, o);
-        if (kSplits > 1) {
-          float acc[32];
+        for (int i = 0; i < 32; ++i) acc[i] = 0.f;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+        for (int s2 = 0; s2 < kSplits; ++s2) {
+          if (s2 == sp) {
 #pragma unroll
-          for (int s2 = 0; s2 < kSplits; ++s2) {
-            if (s2 == sp) {
+            for (int i = 0; i < 32; ++i) acc[i] = fmaf(w[s2], o[i], acc[i]);
+          } else {
+            const uint8_t* src = smraw + (s2 < sp ? s2 : s2 - 1) * (size_t)Mg::kPart + (size_t)col * 512 + l * 16;
 #pragma unroll
-              for (int i = 0; i < 32; ++i) acc[i] = fmaf(w[s2], o[i], acc[i]);
-            } else {
-              const int slot = s2 < sp ? s2 : s2 - 1;
-              const float4* src = reinterpret_cast<const float4*>(smraw + (size_t)slot * kCols * 512) +
-                                  (kMine * cw + 32 * cc) / 4 * 128 + l;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 v = src[i * 128];
-                acc[4 * i] = fmaf(w[s2], v.x, acc[4 * i]);
-                acc[4 * i + 1] = fmaf(w[s2], v.y, acc[4 * i + 1]);
-                acc[4 * i + 2] = fmaf(w[s2], v.z, acc[4 * i + 2]);
-                acc[4 * i + 3] = fmaf(w[s2], v.w, acc[4 * i + 3]);
-              }
+            for (int i = 0; i < 8; ++i) {
+              const float4 x = *reinterpret_cast<const float4*>(src + i * 2048);
+              acc[4 * i] = fmaf(w[s2], x.x, acc[4 * i]);
+              acc[4 * i + 1] = fmaf(w[s2], x.y, acc[4 * i + 1]);
+              acc[4 * i + 2] = fmaf(w[s2], x.z, acc[4 * i + 2]);
+              acc[4 * i + 3] = fmaf(w[s2], x.w, acc[4 * i + 3]);
             }
           }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = acc[i];
         }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = bad ? 0.f : acc[i];
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<uint4*>(stg + hl * 1024 + (((32 * half + col / 8 + q) ^ (hl & 31)) << 4)) = pack8(&o[8 * q], inv);
+      for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(stg + 2 * col + 16 * q) = pack8(&o[8 * q], inv);
     }
-    const int head = kHc * (int)rank + hl;
-    if (a.lse && sp == 0 && cw == 0 && half == 0 && head < a.n_heads)
-      a.lse[(int64_t)t * a.n_heads + head] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    fence_proxy_async_smem();
     named_bar_sync(1, kSmThreads);
-    // this pair's pieces of each head: kCols / 8 from each half of the dims
-    const int heads_here = max(0, min(kHc, a.n_heads - kHc * (int)rank));
-    uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + ((int64_t)t * a.n_heads + kHc * (int)rank) * kDC);
-    constexpr int kSeg = kCols / 8;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < heads_here * 2 * kSeg; i += kSmThreads) {
-      const int h = i / (2 * kSeg), r = i % (2 * kSeg), ch = (r / kSeg) * 32 + sp * kSeg + r % kSeg;
-      out[h * 64 + ch] = *reinterpret_cast<const uint4*>(stg + h * 1024 + ((ch ^ (h & 31)) << 4));
+    const int head = kHc * (int)rank + hl;
+    if (cw == 0 && head < a.n_heads) {
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((int64_t)t * a.n_heads + head) * kDC + 256 * half + sp * kCols;
+      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(out), "r"(smem_u32(stg)), "n"(2 * kCols)
+                   : "memory");
+      bulk_commit();
+      if (a.lse && sp == 0 && half == 0)
+        a.lse[(int64_t)t * a.n_heads + head] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
     }
+    // this thread's copies are done before shared memory goes
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();

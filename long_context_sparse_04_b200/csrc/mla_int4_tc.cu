@@ -33,9 +33,11 @@
 //                lane + 64.  The running maximum passes from group to group through
 //                shared memory (a few hundred cycles a block); each thread keeps its
 //                own sum.  Lazy rescale as in mla_tc.cu.
-//   warps 8-15   decode the keys' tile: packed pieces from global memory to
-//                registers one block ahead, then 16-byte stores, swizzled
-//   warps 16-23  decode the values' tile, the same way
+//   warps 8-23   decode, two groups of eight warps that take the blocks in turn, each
+//                with its own stage: packed pieces from global memory to registers, two
+//                blocks' time ahead of their use (one block's was too little: the loads
+//                set the pace), then 16-byte stores, swizzled, of the keys' and the
+//                values' tile
 //   warp 24      tensor memory; in the pair's first CTA one thread issues the MMAs
 //   warp 25      resolves the selection to cache rows, two blocks at a time
 // Tiles, weights and logits have two stages each; S of block j+1 is issued before
@@ -57,7 +59,7 @@ constexpr int kBlk = 64, kHalfBlk = 32;
 constexpr int kMaxKeys = 2048;
 constexpr int kMaxPairs = 4;                    // key splits of a row: 1, 2 or 4 (a cluster of 8 CTAs)
 constexpr int kSmWarps = 8, kDecWarps = 8;
-constexpr int kKWarp0 = 8, kVWarp0 = 16, kMmaWarp = 24, kRowWarp = 25;
+constexpr int kDecWarp0 = 8, kMmaWarp = 24, kRowWarp = 25;
 constexpr int kThreads = 32 * 26;
 constexpr int kSmThreads = 32 * kSmWarps;
 constexpr int kDecThreads = 2 * kDecWarps * 32;
@@ -307,108 +309,106 @@ __device__ __forceinline__ void resolve_rows(Smem& S, const MlaArgs& a, int t, i
 }
 
 // ---------------------------------------------------------------- decoding
-// A warp's share of one block: two pieces of 32 dims of one key per lane.  Eight
-// neighbouring lanes take eight keys (their 16-byte stores fall into distinct
-// banks of the swizzled tile), the four lane groups four neighbouring pieces (64
-// bytes of codes of one key: two whole sectors).
-//   keys' tile:   warp w takes keys 8 (w % 4).., pieces 4 (w / 4).. and 8 further on
-//   values' tile: warp w takes keys 8 w..,       pieces 0.. and 4 further on
-template <bool kV>
-struct Decoder {
-  static constexpr int kChunk = (kV ? kBlk : kHalfBlk) * 128;    // bytes of 64 dims of the tile
-  static constexpr int kNext = kV ? 4 : 8;                       // pieces from a lane's first to its second
-  struct Pieces {
-    uint4 codes[2], rope;
-    uint32_t scales[2];
-  };
-  int key, src_codes, src_scales, rope_key, rope_src;            // of the lane: key in the block, byte offsets in the row
-  uint32_t dst[4], rope_dst;                                     // shared-memory offsets in a tile
+// Two pieces of 32 dims of one key's codes, with their four scales.
+struct Pieces {
+  uint4 codes[2];
+  uint32_t scales[2];
 
-  __device__ __forceinline__ Decoder(int wt, uint32_t rank) {
-    const int lane = threadIdx.x & 31, low = lane & 7, grp = lane >> 3;
-    const int in_tile = (kV ? wt : wt & 3) * 8 + low, piece = (kV ? 0 : (wt >> 2) * 4) + grp;
-    key = in_tile + (kV ? 0 : kHalfBlk * (int)rank);
-    src_codes = 16 * (piece + (kV ? 8 * (int)rank : 0));
-    src_scales = kRow.scale + 2 * (piece + (kV ? 8 * (int)rank : 0));
-#pragma unroll
-    for (int e = 0; e < 4; ++e) dst[e] = (piece >> 1) * kChunk + sw128_off(in_tile, (piece & 1) * 4 + e);
-    const int kt = wt * 32 + lane;                               // RoPE: 32 keys x 8 pieces, one per thread
-    rope_key = (kt >> 3) + kHalfBlk * (int)rank;
-    rope_src = kRow.rope + 16 * (kt & 7);
-    rope_dst = 8 * kChunk + sw128_off(kt >> 3, kt & 7);
-  }
-  // Loads a block's packed pieces of cache rows `row` (codes) and `rrow` (RoPE key);
-  // zeros for a key without a row.
-  __device__ __forceinline__ void load(Pieces& x, int row, int rrow, const uint8_t* latent) const {
-    x.codes[0] = x.codes[1] = x.rope = make_uint4(0u, 0u, 0u, 0u);
-    x.scales[0] = x.scales[1] = 0u;
+  // Pieces at byte `codes_at` and `kNext` pieces further on, scales likewise; zeros for
+  // a key without a row.
+  template <int kNext>
+  __device__ __forceinline__ void load(const uint8_t* latent, int row, int codes_at, int scales_at) {
+    codes[0] = codes[1] = make_uint4(0u, 0u, 0u, 0u);
+    scales[0] = scales[1] = 0u;
     if (row >= 0) {
       const uint8_t* src = latent + (int64_t)row * kRow.bytes;
-      x.codes[0] = __ldg(reinterpret_cast<const uint4*>(src + src_codes));
-      x.codes[1] = __ldg(reinterpret_cast<const uint4*>(src + src_codes + 16 * kNext));
-      x.scales[0] = __ldg(reinterpret_cast<const unsigned short*>(src + src_scales));
-      x.scales[1] = __ldg(reinterpret_cast<const unsigned short*>(src + src_scales + 2 * kNext));
+      codes[0] = __ldg(reinterpret_cast<const uint4*>(src + codes_at));
+      codes[1] = __ldg(reinterpret_cast<const uint4*>(src + codes_at + 16 * kNext));
+      scales[0] = __ldg(reinterpret_cast<const unsigned short*>(src + scales_at));
+      scales[1] = __ldg(reinterpret_cast<const unsigned short*>(src + scales_at + 2 * kNext));
     }
-    if (!kV && rrow >= 0) x.rope = __ldg(reinterpret_cast<const uint4*>(latent + (int64_t)rrow * kRow.bytes + rope_src));
   }
-  __device__ __forceinline__ void store(const Pieces& x, uint8_t* tile) const {
+  // Decoded into a tile whose rows are at `row`; the second piece `kStep` bytes on.
+  template <int kStep>
+  __device__ __forceinline__ void store(uint8_t* row, const uint32_t (&swz)[4]) const {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      uint8_t* t = tile + i * (kNext / 2) * kChunk;
-      const ScalePair s0 = scale_pair(x.scales[i] & 0xFFu), s1 = scale_pair(x.scales[i] >> 8);
-      *reinterpret_cast<uint4*>(t + dst[0]) = decode_word(x.codes[i].x, s0);
-      *reinterpret_cast<uint4*>(t + dst[1]) = decode_word(x.codes[i].y, s0);
-      *reinterpret_cast<uint4*>(t + dst[2]) = decode_word(x.codes[i].z, s1);
-      *reinterpret_cast<uint4*>(t + dst[3]) = decode_word(x.codes[i].w, s1);
+      const ScalePair s0 = scale_pair(scales[i] & 0xFFu), s1 = scale_pair(scales[i] >> 8);
+      *reinterpret_cast<uint4*>(row + i * kStep + swz[0]) = decode_word(codes[i].x, s0);
+      *reinterpret_cast<uint4*>(row + i * kStep + swz[1]) = decode_word(codes[i].y, s0);
+      *reinterpret_cast<uint4*>(row + i * kStep + swz[2]) = decode_word(codes[i].z, s1);
+      *reinterpret_cast<uint4*>(row + i * kStep + swz[3]) = decode_word(codes[i].w, s1);
     }
-    if (!kV) *reinterpret_cast<uint4*>(tile + rope_dst) = x.rope;
   }
 };
 
-template <bool kV>
-__device__ __forceinline__ void decode_blocks(Smem& S, const MlaArgs& a, int nblk, uint32_t rank, uint32_t first, int wt) {
+// The blocks of one parity g: warp w of its eight.  Per block a lane decodes two
+// pieces of the keys' tile and two of the values'.  Eight neighbouring lanes take
+// eight keys (their 16-byte stores fall into distinct banks of the swizzled tile),
+// the four lane groups four neighbouring pieces (64 bytes of codes of one key: two
+// whole sectors).
+//   keys' tile:   keys 8 (w % 4).. of the CTA's 32, pieces 4 (w / 4).. and 8 further on
+//   values' tile: keys 8 w.., pieces 0.. of the CTA's 8 and 4 further on
+__device__ __forceinline__ void decode_blocks(Smem& S, const MlaArgs& a, int nblk, uint32_t rank, uint32_t first, int w, int g) {
   const uint8_t* latent = static_cast<const uint8_t*>(a.latent);
-  const Decoder<kV> dec(wt, rank);
-  typename Decoder<kV>::Pieces even, odd;         // the packed pieces of even and odd blocks
-  const bool stamp = a.trace != nullptr && wt == 0 && (threadIdx.x & 31) == 0;
-  int row[2] = {-1, -1}, rrow[2] = {-1, -1};      // of the two blocks handed over last
-  const auto take_rows = [&](int p) {
-    if (!wait_warp(&S.rows_full[p & 1], (p >> 1) & 1, a.status, 54)) return false;
+  const int lane = threadIdx.x & 31, low = lane & 7, grp = lane >> 3;
+  const bool stamp = a.trace != nullptr && w == 0 && lane == 0;
+  uint32_t swz[4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      row[u] = S.rows[p & 1][u * kBlk + dec.key];
-      if (!kV) rrow[u] = S.rows[p & 1][u * kBlk + dec.rope_key];
-    }
+  for (int e = 0; e < 4; ++e) swz[e] = (((grp & 1) * 4 + e) ^ low) << 4;
+  constexpr int kKChunk = kHalfBlk * 128, kVChunk = kBlk * 128;   // bytes of 64 dims of a tile
+  const int k_key = (w & 3) * 8 + low, k_piece = (w >> 2) * 4 + grp;
+  const int v_key = w * 8 + low, v_piece = 8 * (int)rank + grp;
+  uint8_t* k_dst = S.k[g][0] + (k_piece >> 1) * kKChunk + k_key * 128;
+  uint8_t* v_dst = S.v[g][0] + (grp >> 1) * kVChunk + v_key * 128;
+  const int kt = w * 32 + lane;                                   // RoPE: 32 keys x 8 pieces, one per thread
+  uint8_t* r_dst = S.k[g][8] + sw128_off(kt >> 3, kt & 7);
+  const int own = g * kBlk + kHalfBlk * (int)rank;                // the CTA's keys in the two blocks' rows
+  Pieces kp, vp;
+  uint4 rope;
+  int k_row = -1, v_row = -1;
+  const auto load_keys = [&](int j) {
+    const int p = j >> 1;
+    if (!wait_warp(&S.rows_full[p & 1], (p >> 1) & 1, a.status, 54)) return false;
+    const int32_t* rows = S.rows[p & 1];
+    k_row = rows[own + k_key];
+    v_row = rows[g * kBlk + v_key];
+    const int r_row = rows[own + (kt >> 3)];
     warp_arrive(&S.rows_free[p & 1]);
+    kp.load<8>(latent, k_row, 16 * k_piece, kRow.scale + 2 * k_piece);
+    rope = make_uint4(0u, 0u, 0u, 0u);
+    if (r_row >= 0) rope = __ldg(reinterpret_cast<const uint4*>(latent + (int64_t)r_row * kRow.bytes + kRow.rope + 16 * (kt & 7)));
     return true;
   };
-  const auto block = [&](int j, const typename Decoder<kV>::Pieces& now) {
-    const int b = j & 1;
-    // the stage is free once the products of block j-2 have read it
-    if (!wait_warp(kV ? &S.pv_done[b] : &S.s_full[b], ((j >> 1) & 1) ^ 1, a.status, kV ? 48 : 47)) return false;
-    if (stamp) tstamp(a.trace, rank, kV ? 7 : 5, j);
-    dec.store(now, kV ? S.v[b][0] : S.k[b][0]);
-    fence_proxy_async_smem();                     // generic stores -> tensor cores
-    warp_arrive_first(kV ? &S.v_full[b] : &S.k_full[b], first);
-    if (stamp) tstamp(a.trace, rank, kV ? 1 : 0, j);
-    return true;
-  };
-  bool ok = take_rows(0);
-  dec.load(even, row[0], rrow[0], latent);
+  const auto load_values = [&] { vp.load<4>(latent, v_row, 16 * v_piece, kRow.scale + 2 * v_piece); };
+  bool ok = true;
+  if (g < nblk) {
+    ok = load_keys(g);
+    load_values();
+  }
   cp_async_wait_all();                            // this thread's pieces of Q
   fence_proxy_async_smem();
   cluster_wait();                                 // the first CTA's barriers are initialised
   warp_arrive_first(&S.q_full, first);
-  for (int j = 0; ok && j < nblk; j += 2) {
-    if (j + 1 < nblk) dec.load(odd, row[1], rrow[1], latent);
-    ok = block(j, even);
-    if (!ok || j + 1 >= nblk) break;
-    if (j + 2 < nblk) {
-      ok = take_rows((j >> 1) + 1);
-      if (!ok) break;
-      dec.load(even, row[0], rrow[0], latent);
-    }
-    ok = block(j + 1, odd);
+  for (int j = g; ok && j < nblk; j += 2) {
+    const uint32_t free = ((j >> 1) & 1) ^ 1;
+    // the keys' stage is free once S of block j-2 has read it
+    if (!wait_warp(&S.s_full[g], free, a.status, 47)) break;
+    if (stamp) tstamp(a.trace, rank, 5, j);
+    kp.store<4 * kKChunk>(k_dst, swz);
+    *reinterpret_cast<uint4*>(r_dst) = rope;
+    fence_proxy_async_smem();                     // generic stores -> tensor cores
+    warp_arrive_first(&S.k_full[g], first);
+    if (stamp) tstamp(a.trace, rank, 0, j);
+    if (j + 2 < nblk) ok = load_keys(j + 2);
+    // the values' once P V of block j-2 has
+    if (!ok || !wait_warp(&S.pv_done[g], free, a.status, 48)) break;
+    if (stamp) tstamp(a.trace, rank, 7, j);
+    vp.store<2 * kVChunk>(v_dst, swz);
+    fence_proxy_async_smem();
+    warp_arrive_first(&S.v_full[g], first);
+    if (stamp) tstamp(a.trace, rank, 1, j);
+    if (j + 2 < nblk) load_values();
   }
 }
 
@@ -606,19 +606,19 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(MlaArgs a) {
   } else if (warp == kRowWarp) {
     if (!empty) resolve_rows(S, a, t, seq, klen, k0, nvalid, nblk);
     else cluster_wait();
-  } else if (warp >= kKWarp0) {
+  } else if (warp >= kDecWarp0) {
     if (!empty) {
       // Q lands while the selection is resolved; heads beyond H are zeros
-      const int g = threadIdx.x - 32 * kKWarp0, h0 = kHc * (int)rank;
+      const int th = threadIdx.x - 32 * kDecWarp0, h0 = kHc * (int)rank;
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)t * a.n_heads * kD;
 #pragma unroll
       for (int i = 0; i < kHc * kD / 8 / kDecThreads; ++i) {
-        const int qi = g + i * kDecThreads, h = qi / (kD / 8), c = qi - h * (kD / 8);
+        const int qi = th + i * kDecThreads, h = qi / (kD / 8), c = qi - h * (kD / 8);
         const bool in = h0 + h < a.n_heads;
         cp_async_16_zfill(S.q[c >> 3] + sw128_off(h, c & 7), q + (int64_t)(in ? h0 + h : 0) * kD + 8 * c, in);
       }
-      if (warp >= kVWarp0) decode_blocks<true>(S, a, nblk, rank, to_first, warp - kVWarp0);
-      else decode_blocks<false>(S, a, nblk, rank, to_first, warp - kKWarp0);
+      const int w = warp - kDecWarp0;
+      decode_blocks(S, a, nblk, rank, to_first, w % kDecWarps, w / kDecWarps);
     } else {
       cluster_wait();
     }

@@ -110,6 +110,11 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   return false;
 }
 
+__device__ __forceinline__ void st_smem_v4(uint32_t saddr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
 // ---------------------------------------------------------------- programmatic dependent launch
 // Kernels of one call are launched with programmatic stream serialization:
 // a kernel may start while its predecessor in the stream is still running.

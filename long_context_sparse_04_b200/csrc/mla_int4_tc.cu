@@ -309,62 +309,58 @@ __device__ __forceinline__ void resolve_rows(Smem& S, const MlaArgs& a, int t, i
 }
 
 // ---------------------------------------------------------------- decoding
-// Two pieces of 32 dims of one key's codes, with their four scales.
-struct Pieces {
+// The packed codes of 64 dims of one key (32 bytes) and their four scales, first and
+// second half swapped in odd units.
+struct Unit {
   uint4 codes[2];
-  uint32_t scales[2];
+  uint32_t scales;
 
-  // Pieces at byte `codes_at` and `kNext` pieces further on, scales likewise; zeros for
-  // a key without a row.
-  template <int kNext>
-  __device__ __forceinline__ void load(const uint8_t* latent, int row, int codes_at, int scales_at) {
+  // Unit `u` of the row (zeros for a key without a row).
+  __device__ __forceinline__ void load(const uint8_t* latent, int row, int u) {
     codes[0] = codes[1] = make_uint4(0u, 0u, 0u, 0u);
-    scales[0] = scales[1] = 0u;
+    scales = 0u;
     if (row >= 0) {
       const uint8_t* src = latent + (int64_t)row * kRow.bytes;
-      codes[0] = __ldg(reinterpret_cast<const uint4*>(src + codes_at));
-      codes[1] = __ldg(reinterpret_cast<const uint4*>(src + codes_at + 16 * kNext));
-      scales[0] = __ldg(reinterpret_cast<const unsigned short*>(src + scales_at));
-      scales[1] = __ldg(reinterpret_cast<const unsigned short*>(src + scales_at + 2 * kNext));
+      const int odd = (u & 1) * 16;
+      codes[0] = __ldg(reinterpret_cast<const uint4*>(src + 32 * u + odd));
+      codes[1] = __ldg(reinterpret_cast<const uint4*>(src + 32 * u + (odd ^ 16)));
+      scales = __ldg(reinterpret_cast<const uint32_t*>(src + kRow.scale) + u);
     }
   }
-  // Decoded into a tile whose rows are at `row`; the second piece `kStep` bytes on.
-  template <int kStep>
-  __device__ __forceinline__ void store(uint8_t* row, const uint32_t (&swz)[4]) const {
+  // Decoded to a tile's 128-byte row; `at`: its address with the swizzle of the first
+  // piece in bits 4-6, from which piece e's differs by e (the tile's rows and bits are
+  // aligned, so that an exclusive or does).
+  __device__ __forceinline__ void store(uint32_t at, int odd) const {
+    const uint32_t sc = odd ? __funnelshift_r(scales, scales, 16) : scales;
+    const uint32_t w[8] = {codes[0].x, codes[0].y, codes[0].z, codes[0].w, codes[1].x, codes[1].y, codes[1].z, codes[1].w};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const ScalePair s0 = scale_pair(scales[i] & 0xFFu), s1 = scale_pair(scales[i] >> 8);
-      *reinterpret_cast<uint4*>(row + i * kStep + swz[0]) = decode_word(codes[i].x, s0);
-      *reinterpret_cast<uint4*>(row + i * kStep + swz[1]) = decode_word(codes[i].y, s0);
-      *reinterpret_cast<uint4*>(row + i * kStep + swz[2]) = decode_word(codes[i].z, s1);
-      *reinterpret_cast<uint4*>(row + i * kStep + swz[3]) = decode_word(codes[i].w, s1);
+    for (int q = 0; q < 4; ++q) {
+      const ScalePair s = scale_pair((sc >> (8 * q)) & 0xFFu);
+      st_smem_v4(at ^ (32u * q), decode_word(w[2 * q], s));
+      st_smem_v4(at ^ (32u * q + 16u), decode_word(w[2 * q + 1], s));
     }
   }
 };
 
-// The blocks of one parity g: warp w of its eight.  Per block a lane decodes two
-// pieces of the keys' tile and two of the values'.  Eight neighbouring lanes take
-// eight keys (their 16-byte stores fall into distinct banks of the swizzled tile),
-// the four lane groups four neighbouring pieces (64 bytes of codes of one key: two
-// whole sectors).
-//   keys' tile:   keys 8 (w % 4).. of the CTA's 32, pieces 4 (w / 4).. and 8 further on
-//   values' tile: keys 8 w.., pieces 0.. of the CTA's 8 and 4 further on
+// The blocks of one parity g: warp w of its eight.  Per block a lane decodes one unit
+// of the keys' tile and one of the values'.  Eight neighbouring lanes take four keys
+// and two neighbouring units of each: a load then touches four lines for every eight
+// lanes (eight keys touched eight, and the L1's data stage set the pace), and with
+// odd units' halves swapped the eight 16-byte stores still fall into distinct banks.
+//   keys' tile:   keys 4 w.. of the CTA's 32, all 8 units
+//   values' tile: keys 8 w.., the CTA's 4 units
 __device__ __forceinline__ void decode_blocks(Smem& S, const MlaArgs& a, int nblk, uint32_t rank, uint32_t first, int w, int g) {
   const uint8_t* latent = static_cast<const uint8_t*>(a.latent);
-  const int lane = threadIdx.x & 31, low = lane & 7, grp = lane >> 3;
+  const int lane = threadIdx.x & 31, odd = lane & 1, quad = lane >> 3;
   const bool stamp = a.trace != nullptr && w == 0 && lane == 0;
-  uint32_t swz[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) swz[e] = (((grp & 1) * 4 + e) ^ low) << 4;
-  constexpr int kKChunk = kHalfBlk * 128, kVChunk = kBlk * 128;   // bytes of 64 dims of a tile
-  const int k_key = (w & 3) * 8 + low, k_piece = (w >> 2) * 4 + grp;
-  const int v_key = w * 8 + low, v_piece = 8 * (int)rank + grp;
-  uint8_t* k_dst = S.k[g][0] + (k_piece >> 1) * kKChunk + k_key * 128;
-  uint8_t* v_dst = S.v[g][0] + (grp >> 1) * kVChunk + v_key * 128;
+  const int k_key = 4 * w + ((lane & 7) >> 1), k_unit = 2 * quad + odd;
+  const int v_key = 8 * w + 4 * (quad & 1) + ((lane & 7) >> 1), v_unit = 2 * (quad >> 1) + odd;
+  const uint32_t k_dst = smem_u32(S.k[g][k_unit]) + k_key * 128 + (((4 * odd) ^ (k_key & 7)) << 4);
+  const uint32_t v_dst = smem_u32(S.v[g][v_unit]) + v_key * 128 + (((4 * odd) ^ (v_key & 7)) << 4);
   const int kt = w * 32 + lane;                                   // RoPE: 32 keys x 8 pieces, one per thread
   uint8_t* r_dst = S.k[g][8] + sw128_off(kt >> 3, kt & 7);
   const int own = g * kBlk + kHalfBlk * (int)rank;                // the CTA's keys in the two blocks' rows
-  Pieces kp, vp;
+  Unit ku, vu;
   uint4 rope;
   int k_row = -1, v_row = -1;
   const auto load_keys = [&](int j) {
@@ -375,12 +371,12 @@ __device__ __forceinline__ void decode_blocks(Smem& S, const MlaArgs& a, int nbl
     v_row = rows[g * kBlk + v_key];
     const int r_row = rows[own + (kt >> 3)];
     warp_arrive(&S.rows_free[p & 1]);
-    kp.load<8>(latent, k_row, 16 * k_piece, kRow.scale + 2 * k_piece);
+    ku.load(latent, k_row, k_unit);
     rope = make_uint4(0u, 0u, 0u, 0u);
     if (r_row >= 0) rope = __ldg(reinterpret_cast<const uint4*>(latent + (int64_t)r_row * kRow.bytes + kRow.rope + 16 * (kt & 7)));
     return true;
   };
-  const auto load_values = [&] { vp.load<4>(latent, v_row, 16 * v_piece, kRow.scale + 2 * v_piece); };
+  const auto load_values = [&] { vu.load(latent, v_row, 4 * (int)rank + v_unit); };
   bool ok = true;
   if (g < nblk) {
     ok = load_keys(g);
@@ -395,7 +391,7 @@ __device__ __forceinline__ void decode_blocks(Smem& S, const MlaArgs& a, int nbl
     // the keys' stage is free once S of block j-2 has read it
     if (!wait_warp(&S.s_full[g], free, a.status, 47)) break;
     if (stamp) tstamp(a.trace, rank, 5, j);
-    kp.store<4 * kKChunk>(k_dst, swz);
+    ku.store(k_dst, odd);
     *reinterpret_cast<uint4*>(r_dst) = rope;
     fence_proxy_async_smem();                     // generic stores -> tensor cores
     warp_arrive_first(&S.k_full[g], first);
@@ -404,7 +400,7 @@ __device__ __forceinline__ void decode_blocks(Smem& S, const MlaArgs& a, int nbl
     // the values' once P V of block j-2 has
     if (!ok || !wait_warp(&S.pv_done[g], free, a.status, 48)) break;
     if (stamp) tstamp(a.trace, rank, 7, j);
-    vp.store<2 * kVChunk>(v_dst, swz);
+    vu.store(v_dst, odd);
     fence_proxy_async_smem();
     warp_arrive_first(&S.v_full[g], first);
     if (stamp) tstamp(a.trace, rank, 1, j);

@@ -144,7 +144,8 @@ typedef struct {
  *   contiguous:                  seq_start[b] + s   (seq_start NULL: s)        */
 typedef struct {
   const void* latent;         /* [num_tokens, d_c + d_r] bf16 | f32, row-major,
-                                 or packed rows of dsa_latent_row_bytes (DSA_INT4) */
+                                 or packed rows of dsa_latent_row_bytes (DSA_INT4,
+                                 32-byte aligned)                              */
   const void* idx_k;          /* [num_tokens, d_idx] e4m3 | f32, row-major      */
   const float* idx_k_scale;   /* [num_tokens] (required for e4m3, else NULL)     */
   const int32_t* seq_start;   /* [num_seqs] or NULL (contiguous layout)          */

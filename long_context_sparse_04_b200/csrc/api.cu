@@ -126,7 +126,8 @@ dsa_status check_cache(const dsa_cache* c, const dsa_dims* d, bool need_idx, boo
   }
   if (need_latent) {
     CHECK_ARG(c->latent != nullptr, "latent is NULL");
-    CHECK_ARG(aligned(c->latent, 16), "latent must be 16-byte aligned");
+    CHECK_ARG(aligned(c->latent, d->mla_dtype == DSA_INT4 ? 32 : 16),
+              "latent must be 16-byte aligned (int4: 32-byte)");
   }
   if (c->block_table) {
     CHECK_ARG(c->page_size > 0 && c->max_pages_per_seq > 0, "paged cache needs page_size > 0");

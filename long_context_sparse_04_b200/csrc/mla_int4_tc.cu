@@ -39,12 +39,17 @@
 //                set the pace), then 16-byte stores, swizzled, of the keys' and the
 //                values' tile
 //   warp 24      tensor memory; in the pair's first CTA one thread issues the MMAs
-//   warp 25      resolves the selection to cache rows, two blocks at a time
+//   warp 25      resolves the selection to cache rows, up to four blocks ahead
 // Tiles, weights and logits have two stages each; S of block j+1 is issued before
 // P V of block j, so that the tensor cores work while the softmax of block j runs.
+// Without key splits the kernel is persistent: a pair takes rows t, t + pairs, ...,
+// its blocks one stream across rows (block counter n: stage and group n % 2), so that
+// the next row's selection, rows, tiles and Q come in while this row is finished.
 //
 // Decode batches split a row's keys over 2 or 4 pairs of one cluster, which merge
 // through distributed shared memory: no scratch in global memory, no arrival order.
+#include <cudaTypedefs.h>
+
 #include "dsa_int4.cuh"
 #include "dsa_kernels.cuh"
 #include "mla_common.cuh"
@@ -65,6 +70,10 @@ constexpr int kSmThreads = 32 * kSmWarps;
 constexpr int kDecThreads = 2 * kDecWarps * 32;
 constexpr int kQChunks = kD / 64;               // 64-dim SW128 chunks: 8 latent, 1 RoPE
 constexpr uint32_t kColS = 0, kColO = 64, kTmemCols = 512;
+// Blocks in the ring of resolved rows, and in that of their validity bits: block n's are
+// read by the softmax after S of block n, and resolving block n + 10 waits for weights
+// that come after that read (rows n + 6 loaded, hence S of block n + 2, P V of block n).
+constexpr int kRowRing = 4, kValidRing = 16;
 // polls of a bounded wait (20 ms at least; real waits take microseconds)
 constexpr uint32_t kWaitPolls = 1u << 20;
 
@@ -75,14 +84,15 @@ struct Smem {                                   // 1024-byte aligned
   uint8_t p[2][kHc * 128];                      // its heads' weights of 64 keys
   float red[2][2 * kHc];                        // by softmax group and lane: block maxima; the final sums
   float m_run[2][kHc];                          // running maximum of a head after a group's block
-  int32_t rows[2][2 * kBlk];                    // cache row per key of two blocks, -1 = none
-  uint32_t valid[kMaxKeys / 32];                // per 32 keys: bit i set = key i has a row
+  int32_t rows[kRowRing][kBlk];                 // cache row per key of a block, -1 = none
+  uint32_t valid[kValidRing][2];                // per 32 keys: bit i set = key i has a row
   // waited for by the issuing thread, in the pair's first CTA
-  uint64_t q_full, k_full[2], v_full[2], p_full[2];
+  uint64_t q_full, k_full[2], v_full[2], p_full[2], o_free;
   // arrivals of finished products, in both CTAs
   uint64_t s_full[2], pv_done[2];
-  uint64_t rows_full[2], rows_free[2];
+  uint64_t rows_full[kRowRing], rows_free[kRowRing];
   uint64_t merged;                              // the other splits' parts have arrived
+  uint64_t v_idle[2];                           // the row's output has left a stage of the values' tiles
   uint64_t drained;
   uint32_t tmem_base;
 };
@@ -91,16 +101,70 @@ static_assert(offsetof(Smem, k) % 1024 == 0 && offsetof(Smem, v) % 1024 == 0 && 
 // The merge of a row's key splits S: pair s finishes columns [256 s / S, 256 (s + 1) / S)
 // of every lane and gets them from the other pairs, [source][column / 4][lane] float4,
 // where Q lay, with (max, sum) per source and head; it sends its other columns from
-// behind that.  Rows of the finished output are staged behind those.
+// behind that.  Finished columns are staged as tiles of 64 heads x 64 dims (128-byte
+// rows, swizzled), one bulk tensor store each: in the values' tiles, idle between a
+// row's last product and the next row's first, or with splits behind what is sent.
 constexpr size_t kRecvMl = 3 * 32768, kSendMl = kRecvMl + kMaxPairs * kHc * 8, kSend = kRecvMl + 4096;
 template <int kSplits>
 struct Merge {
   static constexpr int kCols = 256 / kSplits;                   // columns of a lane that a pair finishes
   static constexpr uint32_t kPart = kCols * 512, kMl = kHc * 8; // bytes of one source's part
-  static constexpr size_t kOut = kSplits == 1 ? offsetof(Smem, v) : kSend + (kSplits - 1) * (size_t)kPart;
-  static constexpr int kOutRow = 4 * kCols + 16;                // bytes of a staged head: odd in 16-byte pieces
+  static constexpr int kTiles = 8 / kSplits;                    // staged tiles: kTiles / 2 from each half of the dims
+  static constexpr size_t kOut =
+      kSplits == 1 ? offsetof(Smem, v) : (kSend + (kSplits - 1) * (size_t)kPart + 1023) / 1024 * 1024;
   static_assert((kSplits - 1) * (size_t)kPart <= kRecvMl, "receive area");
-  static_assert(kOut % 128 == 0 && kOut + kHc * (size_t)kOutRow <= offsetof(Smem, red), "send and output areas");
+  static_assert(kOut + kTiles * 8192 <= offsetof(Smem, p) || (kSplits > 1 && kOut + kTiles * 8192 <= offsetof(Smem, red)),
+                "output tiles");
+  static_assert(kSend + (kSplits - 1) * (size_t)kPart <= offsetof(Smem, red), "send area");
+};
+
+// The selected keys of a row (of its split sp of kSplits).
+struct Row {
+  int klen, seq, nsel, k0, nvalid, nblk;
+};
+template <int kSplits>
+__device__ __forceinline__ Row row_of(const MlaArgs& a, int klen, int seq, int sp) {
+  Row r;
+  const bool known = (seq >= 0 && seq < a.num_seqs) || !a.map.uses_seq();
+  r.klen = klen;
+  r.seq = seq;
+  r.nsel = known ? max(min(klen, a.topk), 0) : 0;
+  // whole blocks per split, shared out over what the row really selects
+  const int per_split = (r.nsel + kSplits * kBlk - 1) / (kSplits * kBlk) * kBlk;
+  r.k0 = sp * per_split;
+  r.nvalid = max(0, min(r.nsel - r.k0, per_split));
+  r.nblk = (r.nvalid + kBlk - 1) / kBlk;
+  return r;
+}
+// The rows t0, t0 + step, ... of a pair, the next one's lengths in flight.
+template <int kSplits>
+struct RowStream {
+  const MlaArgs& a;
+  int t, step, sp, klen_next = 0, seq_next = 0;
+  __device__ __forceinline__ RowStream(const MlaArgs& a_, int t0, int step_, int sp_) : a(a_), t(t0 - step_), step(step_), sp(sp_) {
+    fetch();
+  }
+  __device__ __forceinline__ void fetch() {
+    if (t + step < a.num_rows) {
+      klen_next = __ldg(a.row_klen + t + step);
+      seq_next = __ldg(a.row_seq + t + step);
+    }
+  }
+  // The next row; false behind the last.
+  __device__ __forceinline__ bool next(Row& r) {
+    t += step;
+    if (t >= a.num_rows) return false;
+    r = row_of<kSplits>(a, klen_next, seq_next, sp);
+    fetch();
+    return true;
+  }
+  // The next row that selects anything (r.nblk = 0 behind the last).
+  __device__ __forceinline__ bool next_busy(Row& r) {
+    while (next(r))
+      if (r.nblk > 0) return true;
+    r.nblk = 0;
+    return false;
+  }
 };
 
 // ---------------------------------------------------------------- two-CTA tcgen05
@@ -188,46 +252,55 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
 }
 
 // ---------------------------------------------------------------- MMA issue (first CTA, one thread)
-__device__ __forceinline__ void issue_products(Smem& S, const MlaArgs& a, uint32_t tmem, int nblk, uint16_t mask) {
+template <int kSplits>
+__device__ __forceinline__ void issue_products(Smem& S, RowStream<kSplits> rows, uint32_t tmem, uint16_t mask) {
+  const MlaArgs& a = rows.a;
   DeviceStatus* status = a.status;
   constexpr uint32_t idesc_s = idesc_bf16(kBlk, false);
   constexpr uint32_t idesc_pv = idesc_bf16(256, true);
-  bool ok = wait_local(&S.q_full, 0, status, 41);
   // descriptors: a byte offset within the tile adds offset >> 4 to the address field
   const uint64_t qd = sdesc_sw128(smem_u32(S.q), 16, 1024), pd = sdesc_sw128(smem_u32(S.p), 16, 1024);
   const uint64_t kd0 = sdesc_sw128(smem_u32(S.k[0]), 16, 1024);
   const uint64_t vd0 = sdesc_sw128(smem_u32(S.v[0]), kBlk * 128, 1024);
-  for (int j = 0; ok && j <= nblk; ++j) {
-    if (j < nblk) {
-      const int b = j & 1;
-      // (S of block j-2 has been read: P V of that block waited for its weights)
-      if (!(ok = wait_local(&S.k_full[b], (j >> 1) & 1, status, 42))) break;
-      tc_fence_after();
-      const uint64_t kd = kd0 + (uint64_t)(b * (sizeof(S.k[0]) >> 4));
-      const uint32_t d = tmem + kColS + b * 32;
+  Row r;
+  bool ok = true;
+  uint32_t busy = 0;                              // rows with keys so far
+  for (int n0 = 0; ok && rows.next_busy(r); n0 += r.nblk, ++busy) {
+    ok = wait_local(&S.q_full, busy & 1, status, 41);
+    for (int j = 0; ok && j <= r.nblk; ++j) {
+      if (j < r.nblk) {
+        const int n = n0 + j, b = n & 1;
+        // (S of block n-2 has been read: P V of that block waited for its weights)
+        if (!(ok = wait_local(&S.k_full[b], (n >> 1) & 1, status, 42))) break;
+        tc_fence_after();
+        const uint64_t kd = kd0 + (uint64_t)(b * (sizeof(S.k[0]) >> 4));
+        const uint32_t d = tmem + kColS + b * 32;
 #pragma unroll
-      for (int ch = 0; ch < kQChunks; ++ch)
+        for (int ch = 0; ch < kQChunks; ++ch)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_bf16_pair(d, qd + (ch * kHc * 128 + 32 * kk >> 4), kd + (ch * kHalfBlk * 128 + 32 * kk >> 4), idesc_s,
+                          (ch | kk) != 0);
+        mma_commit_pair(&S.s_full[b], mask);
+        tstamp(a.trace, 0, 2, n);
+      }
+      if (j >= 1) {
+        const int n = n0 + j - 1, b = n & 1;
+        ok = wait_local(&S.v_full[b], (n >> 1) & 1, status, 44) && wait_local(&S.p_full[b], (n >> 1) & 1, status, 45);
+        // the row before has been read out of the accumulator
+        if (j == 1 && busy > 0) ok = ok && wait_local(&S.o_free, (busy - 1) & 1, status, 58);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t vd = vd0 + (uint64_t)(b * (sizeof(S.v[0]) >> 4));
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_bf16_pair(d, qd + (ch * kHc * 128 + 32 * kk >> 4), kd + (ch * kHalfBlk * 128 + 32 * kk >> 4), idesc_s,
-                        (ch | kk) != 0);
-      mma_commit_pair(&S.s_full[b], mask);
-      tstamp(a.trace, 0, 2, j);
-    }
-    if (j >= 1) {
-      const int jj = j - 1, b = jj & 1;
-      ok = wait_local(&S.v_full[b], (jj >> 1) & 1, status, 44) && wait_local(&S.p_full[b], (jj >> 1) & 1, status, 45);
-      if (!ok) break;
-      tc_fence_after();
-      const uint64_t vd = vd0 + (uint64_t)(b * (sizeof(S.v[0]) >> 4));
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-          mma_bf16_pair(tmem + kColO + n * 128, pd + b * (sizeof(S.p[0]) >> 4) + (32 * kk >> 4),
-                        vd + (n * 2 * kBlk * 128 + kk * 16 * 128 >> 4), idesc_pv, (jj | kk) != 0);
-      mma_commit_pair(&S.pv_done[b], mask);
-      tstamp(a.trace, 0, 3, jj);
+          for (int h = 0; h < 2; ++h)
+            mma_bf16_pair(tmem + kColO + h * 128, pd + b * (sizeof(S.p[0]) >> 4) + (32 * kk >> 4),
+                          vd + (h * 2 * kBlk * 128 + kk * 16 * 128 >> 4), idesc_pv, ((j - 1) | kk) != 0);
+        mma_commit_pair(&S.pv_done[b], mask);
+        tstamp(a.trace, 0, 3, n);
+      }
     }
   }
   // every product issued is done before the pair's shared and tensor memory go
@@ -237,39 +310,65 @@ __device__ __forceinline__ void issue_products(Smem& S, const MlaArgs& a, uint32
 }
 
 // ---------------------------------------------------------------- the selection
-// One warp turns the selection into cache rows, two blocks (four keys a lane) at a
-// time: their block-table entries and the next positions are in flight while the
-// two before are handed over.
-__device__ __forceinline__ void resolve_rows(Smem& S, const MlaArgs& a, int t, int seq, int klen, int k0, int nvalid,
-                                             int nblk) {
-  constexpr int kKeys = 2 * kBlk / 32;
-  const int lane = threadIdx.x & 31;
-  const int32_t* idx = a.idx + (int64_t)t * a.topk + k0;
+// One warp turns the selection into cache rows, two keys of a block per lane: the
+// block-table entries of one block and the positions of the next are in flight while
+// the block before is handed over.
+template <int kSplits>
+__device__ __forceinline__ void resolve_rows(Smem& S, RowStream<kSplits> rows, uint32_t rank) {
+  const MlaArgs& a = rows.a;
   const CacheMap& m = a.map;
-  const int32_t* table = m.block_table ? m.block_table + (int64_t)seq * m.max_pages_per_seq : nullptr;
-  const int64_t start = !m.block_table && m.seq_start ? (int64_t)__ldg(m.seq_start + seq) : 0;
-  const auto positions = [&](int p, int (&s)[kKeys]) {
+  const int lane = threadIdx.x & 31;
+  struct Keys {
+    int s[2], e[2];                               // positions, block-table entries
+    int seq;
+    bool any;                                     // a block at all
+  };
+  Row r;
+  r.nblk = 0;
+  int j = 0;
+  bool more = rows.next_busy(r);
+  const auto positions = [&](Keys& x) {
+    x.any = more;
+    x.s[0] = x.s[1] = -1;
+    x.seq = r.seq;
+    if (!more) return;
+    const int32_t* idx = a.idx + (int64_t)rows.t * a.topk + r.k0;
 #pragma unroll
-    for (int u = 0; u < kKeys; ++u) {
-      const int i = p * 2 * kBlk + 32 * u + lane;
-      s[u] = i < nvalid ? __ldg(idx + i) : -1;
-      if (s[u] >= klen) s[u] = -1;
+    for (int u = 0; u < 2; ++u) {
+      const int i = j * kBlk + 32 * u + lane;
+      if (i < r.nvalid) x.s[u] = __ldg(idx + i);
+      if (x.s[u] >= r.klen) x.s[u] = -1;
+    }
+    if (++j == r.nblk) {
+      j = 0;
+      more = rows.next_busy(r);
+      // the next row's Q comes to L2 some blocks before its tile is free: every pair
+      // changes rows at about the same time, and from HBM that took 11,000 cycles
+      const int heads = min(kHc, a.n_heads - kHc * (int)rank);
+      if (more && heads > 0 && lane == 0)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                         static_cast<const __nv_bfloat16*>(a.q) + ((int64_t)rows.t * a.n_heads + kHc * (int)rank) * kD),
+                     "r"(heads * kD * 2) : "memory");
     }
   };
   const auto page_of = [&](int s) { return m.page_shift >= 0 ? s >> m.page_shift : s / m.page_size; };
-  const auto entries = [&](const int (&s)[kKeys], int (&e)[kKeys]) {
+  const auto entries = [&](Keys& x) {
 #pragma unroll
-    for (int u = 0; u < kKeys; ++u) {
-      e[u] = -1;
-      if (s[u] < 0 || table == nullptr) continue;
-      const int pg = page_of(s[u]);
-      if (pg < m.max_pages_per_seq) e[u] = __ldg(table + pg);
-      else set_status(a.status, DSA_ERR_OUT_OF_RANGE, s[u]);
+    for (int u = 0; u < 2; ++u) {
+      x.e[u] = -1;
+      if (x.s[u] < 0) continue;
+      if (m.block_table != nullptr) {
+        const int pg = page_of(x.s[u]);
+        if (pg < m.max_pages_per_seq) x.e[u] = __ldg(m.block_table + (int64_t)x.seq * m.max_pages_per_seq + pg);
+        else set_status(a.status, DSA_ERR_OUT_OF_RANGE, x.s[u]);
+      } else {
+        x.e[u] = m.seq_start != nullptr ? __ldg(m.seq_start + x.seq) : 0;
+      }
     }
   };
-  const auto row_of = [&](int s, int e) {
+  const auto row = [&](int s, int e) {
     if (s < 0) return -1;
-    if (table != nullptr) {
+    if (m.block_table != nullptr) {
       const int pg = page_of(s);
       if (pg >= m.max_pages_per_seq) return -1;
       if (e < 0 || e >= m.num_pages) {
@@ -278,134 +377,192 @@ __device__ __forceinline__ void resolve_rows(Smem& S, const MlaArgs& a, int t, i
       }
       return (int)((int64_t)e * m.page_size + (s - pg * m.page_size));
     }
-    const int64_t r = start + s;
-    if (r < 0 || r >= m.num_tokens) {
+    const int64_t x = (int64_t)e + s;
+    if (x < 0 || x >= m.num_tokens) {
       set_status(a.status, DSA_ERR_OUT_OF_RANGE, s);
       return -1;
     }
-    return (int)r;
+    return (int)x;
   };
-  int s0[kKeys], s1[kKeys], s2[kKeys], e0[kKeys], e1[kKeys];
-  positions(0, s0);
-  positions(1, s1);
-  entries(s0, e0);
-  cluster_wait();
-  for (int p = 0; 2 * p < nblk; ++p) {
-    positions(p + 2, s2);
-    entries(s1, e1);
-    if (!wait_warp(&S.rows_free[p & 1], ((p >> 1) & 1) ^ 1, a.status, 53)) break;
+  Keys x, y, z;
+  positions(x);
+  positions(y);
+  entries(x);
+  for (int n = 0; x.any; ++n) {
+    positions(z);
+    entries(y);
+    const int slot = n % kRowRing;
+    if (!wait_warp(&S.rows_free[slot], (n / kRowRing & 1) ^ 1, a.status, 53)) break;
 #pragma unroll
-    for (int u = 0; u < kKeys; ++u) {
-      const int row = row_of(s0[u], e0[u]);
-      S.rows[p & 1][32 * u + lane] = row;
-      const uint32_t bits = __ballot_sync(0xffffffffu, row >= 0);
-      if (lane == 0) S.valid[kKeys * p + u] = bits;
-      s0[u] = s1[u];
-      s1[u] = s2[u];
-      e0[u] = e1[u];
+    for (int u = 0; u < 2; ++u) {
+      const int rw = row(x.s[u], x.e[u]);
+      S.rows[slot][32 * u + lane] = rw;
+      const uint32_t bits = __ballot_sync(0xffffffffu, rw >= 0);
+      if (lane == 0) S.valid[n % kValidRing][u] = bits;
     }
-    warp_arrive(&S.rows_full[p & 1]);
+    warp_arrive(&S.rows_full[slot]);
+    x = y;
+    y = z;
   }
 }
 
 // ---------------------------------------------------------------- decoding
-// The packed codes of 64 dims of one key (32 bytes) and their four scales, first and
-// second half swapped in odd units.
-struct Unit {
-  uint4 codes[2];
-  uint32_t scales;
+// The tiles hold dims in an order that suits the decoding: a unit is 64 dims (32 bytes
+// of codes, four scales, one chunk of a tile), and its piece e of 8 dims lies at
+// position e ^ f(unit) of the chunk, f = unit for the keys' tile, 2 unit for the
+// values'.  Q's pieces are placed alike, and the output's columns are put back when
+// they are stored, so the permutation costs nothing; it lets lanes that hold different
+// units of a key store their e-th pieces, in register order, to distinct banks.
+__device__ __forceinline__ int key_piece(int unit, int e) { return e ^ (unit & 7); }
+__device__ __forceinline__ int value_piece(int unit, int e) { return e ^ (2 * (unit & 3)); }
 
-  // Unit `u` of the row (zeros for a key without a row).
+struct Unit {
+  uint32_t codes[8], scales;
+
+  // Unit `u` of the row (zeros for a key without a row).  One 32-byte load: lanes that
+  // share a 128-byte line then take one pass of the L1's data stage (8 a warp; as two
+  // 16-byte loads they took 23, and that stage set the pace).
   __device__ __forceinline__ void load(const uint8_t* latent, int row, int u) {
-    codes[0] = codes[1] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) codes[i] = 0u;
     scales = 0u;
     if (row >= 0) {
       const uint8_t* src = latent + (int64_t)row * kRow.bytes;
-      const int odd = (u & 1) * 16;
-      codes[0] = __ldg(reinterpret_cast<const uint4*>(src + 32 * u + odd));
-      codes[1] = __ldg(reinterpret_cast<const uint4*>(src + 32 * u + (odd ^ 16)));
+      asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(codes[0]), "=r"(codes[1]), "=r"(codes[2]), "=r"(codes[3]), "=r"(codes[4]), "=r"(codes[5]),
+                     "=r"(codes[6]), "=r"(codes[7])
+                   : "l"(src + 32 * u));
       scales = __ldg(reinterpret_cast<const uint32_t*>(src + kRow.scale) + u);
     }
   }
-  // Decoded to a tile's 128-byte row; `at`: its address with the swizzle of the first
-  // piece in bits 4-6, from which piece e's differs by e (the tile's rows and bits are
-  // aligned, so that an exclusive or does).
-  __device__ __forceinline__ void store(uint32_t at, int odd) const {
-    const uint32_t sc = odd ? __funnelshift_r(scales, scales, 16) : scales;
-    const uint32_t w[8] = {codes[0].x, codes[0].y, codes[0].z, codes[0].w, codes[1].x, codes[1].y, codes[1].z, codes[1].w};
+  // Decoded to a tile's 128-byte row; `at`: its address with the first piece's swizzled
+  // position in bits 4-6, from which piece e's differs by e (the tile's rows and bits
+  // are aligned, so that an exclusive or does).
+  __device__ __forceinline__ void store(uint32_t at) const {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const ScalePair s = scale_pair((sc >> (8 * q)) & 0xFFu);
-      st_smem_v4(at ^ (32u * q), decode_word(w[2 * q], s));
-      st_smem_v4(at ^ (32u * q + 16u), decode_word(w[2 * q + 1], s));
+      const ScalePair s = scale_pair((scales >> (8 * q)) & 0xFFu);
+      st_smem_v4(at ^ (32u * q), decode_word(codes[2 * q], s));
+      st_smem_v4(at ^ (32u * q + 16u), decode_word(codes[2 * q + 1], s));
     }
   }
 };
 
 // The blocks of one parity g: warp w of its eight.  Per block a lane decodes one unit
-// of the keys' tile and one of the values'.  Eight neighbouring lanes take four keys
-// and two neighbouring units of each: a load then touches four lines for every eight
-// lanes (eight keys touched eight, and the L1's data stage set the pace), and with
-// odd units' halves swapped the eight 16-byte stores still fall into distinct banks.
-//   keys' tile:   keys 4 w.. of the CTA's 32, all 8 units
-//   values' tile: keys 8 w.., the CTA's 4 units
-__device__ __forceinline__ void decode_blocks(Smem& S, const MlaArgs& a, int nblk, uint32_t rank, uint32_t first, int w, int g) {
+// of the keys' tile and one of the values'.
+//   keys' tile:   keys 4 w.. of the CTA's 32, eight lanes the 8 units of a key
+//   values' tile: keys 8 w.., four lanes the CTA's 4 units of a key
+// All sixteen warps bring in Q, once S of the row before has read it; heads beyond H
+// are zeros.
+template <int kSplits>
+__device__ __forceinline__ void decode_blocks(Smem& S, RowStream<kSplits> rows, uint32_t rank, uint32_t first, int w, int g) {
+  const MlaArgs& a = rows.a;
   const uint8_t* latent = static_cast<const uint8_t*>(a.latent);
-  const int lane = threadIdx.x & 31, odd = lane & 1, quad = lane >> 3;
+  const int lane = threadIdx.x & 31;
   const bool stamp = a.trace != nullptr && w == 0 && lane == 0;
-  const int k_key = 4 * w + ((lane & 7) >> 1), k_unit = 2 * quad + odd;
-  const int v_key = 8 * w + 4 * (quad & 1) + ((lane & 7) >> 1), v_unit = 2 * (quad >> 1) + odd;
-  const uint32_t k_dst = smem_u32(S.k[g][k_unit]) + k_key * 128 + (((4 * odd) ^ (k_key & 7)) << 4);
-  const uint32_t v_dst = smem_u32(S.v[g][v_unit]) + v_key * 128 + (((4 * odd) ^ (v_key & 7)) << 4);
+  const int k_key = 4 * w + (lane >> 3), k_unit = lane & 7;
+  const int v_key = 8 * w + (lane >> 2), v_unit = lane & 3;
+  const uint32_t k_dst = smem_u32(S.k[g][k_unit]) + sw128_off(k_key, key_piece(k_unit, 0));
+  const uint32_t v_dst = smem_u32(S.v[g][v_unit]) + sw128_off(v_key, value_piece(v_unit, 0));
   const int kt = w * 32 + lane;                                   // RoPE: 32 keys x 8 pieces, one per thread
   uint8_t* r_dst = S.k[g][8] + sw128_off(kt >> 3, kt & 7);
-  const int own = g * kBlk + kHalfBlk * (int)rank;                // the CTA's keys in the two blocks' rows
+  const int own = kHalfBlk * (int)rank;                           // the CTA's keys in the block's rows
   Unit ku, vu;
   uint4 rope;
-  int k_row = -1, v_row = -1;
-  const auto load_keys = [&](int j) {
-    const int p = j >> 1;
-    if (!wait_warp(&S.rows_full[p & 1], (p >> 1) & 1, a.status, 54)) return false;
-    const int32_t* rows = S.rows[p & 1];
-    k_row = rows[own + k_key];
-    v_row = rows[g * kBlk + v_key];
-    const int r_row = rows[own + (kt >> 3)];
-    warp_arrive(&S.rows_free[p & 1]);
+  int v_row = -1;
+  const auto load_keys = [&](int n) {
+    const int slot = n % kRowRing;
+    if (!wait_warp(&S.rows_full[slot], n / kRowRing & 1, a.status, 54)) return false;
+    const int k_row = S.rows[slot][own + k_key], r_row = S.rows[slot][own + (kt >> 3)];
+    v_row = S.rows[slot][v_key];
+    warp_arrive(&S.rows_free[slot]);
     ku.load(latent, k_row, k_unit);
     rope = make_uint4(0u, 0u, 0u, 0u);
     if (r_row >= 0) rope = __ldg(reinterpret_cast<const uint4*>(latent + (int64_t)r_row * kRow.bytes + kRow.rope + 16 * (kt & 7)));
     return true;
   };
   const auto load_values = [&] { vu.load(latent, v_row, 4 * (int)rank + v_unit); };
+  const auto load_q = [&](int t) {
+    const int th = (g * kDecWarps + w) * 32 + lane, h0 = kHc * (int)rank;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)t * a.n_heads * kD;
+#pragma unroll 3
+    for (int i = 0; i < kHc * kD / 8 / kDecThreads; ++i) {
+      const int qi = th + i * kDecThreads, h = qi / (kD / 8), c = qi - h * (kD / 8);
+      const bool in = h0 + h < a.n_heads;
+      const int piece = c < kDC / 8 ? key_piece(c >> 3, c & 7) : c & 7;
+      cp_async_16_zfill(S.q[c >> 3] + sw128_off(h, piece), q + (int64_t)(in ? h0 + h : 0) * kD + 8 * c, in);
+    }
+  };
+  // blocks known to come, looked up ahead of their use: a load has one place in the
+  // loop, for where two would meet the compiler moves what was loaded, and waits
+  RowStream<kSplits> ahead = rows;
+  int known = 0;
+  const auto comes = [&](int n) {
+    Row x;
+    while (known <= n && ahead.next_busy(x)) known += x.nblk;
+    return n < known;
+  };
   bool ok = true;
-  if (g < nblk) {
+  Row r;
+  if (comes(0)) load_q(ahead.t);                  // the first row's, while its selection is resolved
+  if (comes(g)) {
     ok = load_keys(g);
     load_values();
   }
-  cp_async_wait_all();                            // this thread's pieces of Q
-  fence_proxy_async_smem();
-  cluster_wait();                                 // the first CTA's barriers are initialised
-  warp_arrive_first(&S.q_full, first);
-  for (int j = g; ok && j < nblk; j += 2) {
-    const uint32_t free = ((j >> 1) & 1) ^ 1;
-    // the keys' stage is free once S of block j-2 has read it
-    if (!wait_warp(&S.s_full[g], free, a.status, 47)) break;
-    if (stamp) tstamp(a.trace, rank, 5, j);
-    ku.store(k_dst, odd);
-    *reinterpret_cast<uint4*>(r_dst) = rope;
-    fence_proxy_async_smem();                     // generic stores -> tensor cores
-    warp_arrive_first(&S.k_full[g], first);
-    if (stamp) tstamp(a.trace, rank, 0, j);
-    if (j + 2 < nblk) ok = load_keys(j + 2);
-    // the values' once P V of block j-2 has
-    if (!ok || !wait_warp(&S.pv_done[g], free, a.status, 48)) break;
-    if (stamp) tstamp(a.trace, rank, 7, j);
-    vu.store(v_dst, odd);
+  const auto q_landed = [&] {
+    cp_async_wait_all();
     fence_proxy_async_smem();
-    warp_arrive_first(&S.v_full[g], first);
-    if (stamp) tstamp(a.trace, rank, 1, j);
-    if (j + 2 < nblk) load_values();
+    warp_arrive_first(&S.q_full, first);
+  };
+  cluster_wait();                                 // the first CTA's barriers are initialised
+  if (known > 0) q_landed();
+  uint32_t busy = 0;                              // rows with keys so far
+  for (int n0 = 0; ok && rows.next_busy(r); n0 += r.nblk, ++busy) {
+    bool q_pending = n0 > 0, first_in_row = true;
+    int n = n0 + ((n0 ^ g) & 1);
+    do {
+      const bool mine = n < n0 + r.nblk;
+      const uint32_t free = ((n >> 1) & 1) ^ 1;
+      if (q_pending) {
+        // Q's tile is free once S of the row before's last block has read it
+        if (!(ok = wait_warp(&S.s_full[(n0 - 1) & 1], ((n0 - 1) >> 1) & 1, a.status, 59))) break;
+        load_q(rows.t);
+      }
+      if (mine) {
+        // the keys' stage is free once S of block n-2 has read it
+        if (!(ok = wait_warp(&S.s_full[g], free, a.status, 47))) break;
+        if (stamp) tstamp(a.trace, rank, 5, n);
+        ku.store(k_dst);
+        *reinterpret_cast<uint4*>(r_dst) = rope;
+        fence_proxy_async_smem();                 // generic stores -> tensor cores
+        warp_arrive_first(&S.k_full[g], first);
+        if (stamp) tstamp(a.trace, rank, 0, n);
+      }
+      if (q_pending) {
+        q_landed();
+        q_pending = false;
+      }
+      const bool more = mine && comes(n + 2);
+      if (more && !(ok = load_keys(n + 2))) break;
+      // the output of the row before has left the values' stage (waited for in every
+      // row, also one without a block of this parity: a parity tells two phases apart,
+      // not three)
+      if (first_in_row && busy > 0 && !(ok = wait_warp(&S.v_idle[g], (busy - 1) & 1, a.status, 60))) break;
+      first_in_row = false;
+      if (mine) {
+        // the values' stage is free once P V of block n-2 has read it
+        if (!(ok = wait_warp(&S.pv_done[g], free, a.status, 48))) break;
+        if (stamp) tstamp(a.trace, rank, 7, n);
+        vu.store(v_dst);
+        fence_proxy_async_smem();
+        warp_arrive_first(&S.v_full[g], first);
+        if (stamp) tstamp(a.trace, rank, 1, n);
+        if (more) load_values();
+      }
+      n += 2;
+    } while (n < n0 + r.nblk);
   }
+  cp_async_wait_all();                            // after a wait that ran out
 }
 
 // 32 columns of this thread's lane of O (zeros when no product was issued).
@@ -444,26 +601,26 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// Softmax state of a thread: lane l of tensor memory (head l % 64, keys 32 (l / 64)..
-// of a block), blocks of its group's parity.
+// Softmax state of a thread for one row: lane l of tensor memory (head l % 64, keys
+// 32 (l / 64).. of a block), blocks of its group's parity.
 struct Softmax {
   float m = -INFINITY, sum = 0.f;                 // maximum (log2 domain) that the sum refers to, sum
   bool dead = false;                              // a wait ran out
 
-  // One block of group g = j % 2.  A thread whose wait ran out (dead) skips its waits
+  // Block j of the row, n = n0 + j of the pair, n % 2 = g.  A thread whose wait ran out (dead) skips its waits
   // and goes on, so that every arrival and collective access stays uniform.
-  __device__ __forceinline__ void block(Smem& S, const MlaArgs& a, uint32_t tmem_lane, int j, int nblk, int g, float c,
+  __device__ __forceinline__ void block(Smem& S, const MlaArgs& a, uint32_t tmem_lane, int n, int j, int nblk, int g, float c,
                                         uint32_t rank, uint32_t first) {
     const int l = threadIdx.x & 127, half = l >> 6, hl = l & 63;
-    const uint32_t phase = (j >> 1) & 1;
+    const uint32_t phase = (n >> 1) & 1;
     dead = dead || !wait_local(&S.s_full[g], phase, a.status, 49);
     tc_fence_after();
-    if (l == 0 && a.trace != nullptr) tstamp(a.trace, rank, 4, j);
+    if (l == 0 && a.trace != nullptr) tstamp(a.trace, rank, 4, n);
     float s[32];
     tmem_ld32(tmem_lane + kColS + g * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
     tmem_wait_ld();
     // masked keys are -inf (a full block needs no test)
-    const uint32_t mask = S.valid[2 * j + half];
+    const uint32_t mask = S.valid[n % kValidRing][half];
     if (mask != 0xFFFFFFFFu) {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
@@ -493,7 +650,7 @@ struct Softmax {
       const float alpha = need ? (m_now == -INFINITY ? 0.f : exp2f(m_now - m_new)) : 1.f;
       if (j > 0) {
         // no product is in flight: block j-1's is done, block j's waits for P below
-        dead = dead || !wait_local(&S.pv_done[g ^ 1], ((j - 1) >> 1) & 1, a.status, 50);
+        dead = dead || !wait_local(&S.pv_done[g ^ 1], ((n - 1) >> 1) & 1, a.status, 50);
         tc_fence_after();
 #pragma unroll 1
         for (int cc = 0; cc < 16; ++cc) {
@@ -540,25 +697,39 @@ struct Softmax {
     float l0, l1;
     split_f32(ls, l0, l1);
     sum += l0 + l1;
-    if (l == 0 && a.trace != nullptr) tstamp(a.trace, rank, 6, j);
+    if (l == 0 && a.trace != nullptr) tstamp(a.trace, rank, 6, n);
   }
 };
 
+// 32 columns (from `col`, of a lane's 256) of head hl, scaled and rounded, into the
+// 128-byte row of its staged tile, the values' permutation undone.
+__device__ __forceinline__ void stage_bf16(uint8_t* tile, int hl, int col, const float (&o)[32], float scale) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    *reinterpret_cast<uint4*>(tile + sw128_off(hl, value_piece(col >> 6, (col >> 3 & 7) + q))) = pack8(&o[8 * q], scale);
+}
+// A staged tile to dims [x, x + 64) of heads [y, y + 64) of row t (heads beyond H are
+// dropped by the tensor map's bounds).
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, const uint8_t* tile, int x, int y, int t) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)), "r"(smem_u32(tile)), "r"(x), "r"(y), "r"(t) : "memory");
+}
+
 // S: key splits of a row = pairs of a cluster.
 template <int kSplits>
-__global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(MlaArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_constant__ MlaArgs a,
+                                                                 const __grid_constant__ CUtensorMap out_map) {
   extern __shared__ __align__(1024) uint8_t smraw[];
   Smem& S = *reinterpret_cast<Smem*>(smraw);
   const int warp = threadIdx.x >> 5;
   const uint32_t crank = cluster_ctarank(), rank = crank & 1u, first = crank & ~1u;
   const int sp = (int)(crank >> 1);
   const uint32_t to_first = mapa(smraw, first) - smem_u32(smraw);
-  const int t = blockIdx.x / (2 * kSplits);
   pdl_launch_dependents();
 
-  // setup that reads no input memory overlaps the predecessor's tail
   if (threadIdx.x == 0) {
     mbar_init(&S.q_full, 2 * 2 * kDecWarps);
+    mbar_init(&S.o_free, 2 * kSmWarps);
     mbar_init(&S.drained, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.k_full[i], 2 * kDecWarps);
@@ -566,8 +737,11 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(MlaArgs a) {
       mbar_init(&S.p_full[i], kSmWarps);         // a group's four warps in each CTA
       mbar_init(&S.s_full[i], 1);
       mbar_init(&S.pv_done[i], 1);
+      mbar_init(&S.v_idle[i], 1);
+    }
+    for (int i = 0; i < kRowRing; ++i) {
       mbar_init(&S.rows_full[i], 1);
-      mbar_init(&S.rows_free[i], 2 * kDecWarps);
+      mbar_init(&S.rows_free[i], kDecWarps);
     }
     mbar_init(&S.merged, 1);
     fence_mbar_init();
@@ -581,80 +755,112 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(MlaArgs a) {
   cluster_arrive();                     // waited for before anything touches another CTA
   const uint32_t tmem = S.tmem_base;
   pdl_wait();
-  trace_kernel(a.status, DSA_KERNEL_MLA_INT4_TC);
-  const int klen = a.row_klen[t];
-  const int seq = a.row_seq[t];
-  const bool known = (seq >= 0 && seq < a.num_seqs) || !a.map.uses_seq();
-  if (!known && klen > 0 && threadIdx.x == 0) set_status(a.status, DSA_ERR_OUT_OF_RANGE, t);
-  const int nsel = known ? min(klen, a.topk) : 0;
-  // whole blocks per split, shared out over what the row really selects
-  const int keys_per_split = (max(nsel, 0) + kSplits * kBlk - 1) / (kSplits * kBlk) * kBlk;
-  const int k0 = sp * keys_per_split;
-  const int nvalid = max(0, min(nsel - k0, keys_per_split));
-  const int nblk = (nvalid + kBlk - 1) / kBlk;
-  const bool empty = nblk == 0;
+  trace_kernel(a.status, kSplits > 1 ? DSA_KERNEL_MLA_INT4_TC | DSA_KERNEL_MLA_COMBINE : DSA_KERNEL_MLA_INT4_TC);
+  // with splits one row per cluster, else the pair's share of the rows
+  RowStream<kSplits> rows(a, blockIdx.x / (2 * kSplits), kSplits > 1 ? a.num_rows : (int)gridDim.x / 2, sp);
+  // what the output needs of the last row (with splits: of the only one)
+  using Mg = Merge<kSplits>;
   Softmax sm;
+  bool empty = true;
+  int last = 0, t_out = 0;
 
   if (warp == kMmaWarp) {
     cluster_wait();
-    if (rank == 0 && !empty && elect_one()) issue_products(S, a, tmem, nblk, (uint16_t)(3u << first));
+    if (rank == 0 && elect_one()) issue_products<kSplits>(S, rows, tmem, (uint16_t)(3u << first));
     __syncwarp();
   } else if (warp == kRowWarp) {
-    if (!empty) resolve_rows(S, a, t, seq, klen, k0, nvalid, nblk);
-    else cluster_wait();
+    resolve_rows<kSplits>(S, rows, rank);
+    cluster_wait();
   } else if (warp >= kDecWarp0) {
-    if (!empty) {
-      // Q lands while the selection is resolved; heads beyond H are zeros
-      const int th = threadIdx.x - 32 * kDecWarp0, h0 = kHc * (int)rank;
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)t * a.n_heads * kD;
-#pragma unroll
-      for (int i = 0; i < kHc * kD / 8 / kDecThreads; ++i) {
-        const int qi = th + i * kDecThreads, h = qi / (kD / 8), c = qi - h * (kD / 8);
-        const bool in = h0 + h < a.n_heads;
-        cp_async_16_zfill(S.q[c >> 3] + sw128_off(h, c & 7), q + (int64_t)(in ? h0 + h : 0) * kD + 8 * c, in);
-      }
-      const int w = warp - kDecWarp0;
-      decode_blocks(S, a, nblk, rank, to_first, w % kDecWarps, w / kDecWarps);
-    } else {
-      cluster_wait();
-    }
+    const int w = warp - kDecWarp0;
+    decode_blocks<kSplits>(S, rows, rank, to_first, w % kDecWarps, w / kDecWarps);
   } else {
     cluster_wait();
     const float c = a.sm_scale * kLog2e;
     const uint32_t tmem_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const int g = warp >> 2;
-    for (int j = g; j < nblk; j += 2) sm.block(S, a, tmem_lane, j, nblk, g, c, rank, to_first);
-    if (!sm.dead && !empty) {
-      sm.dead = !wait_local(&S.pv_done[(nblk - 1) & 1], ((nblk - 1) >> 1) & 1, a.status, 52);
+    const int l = threadIdx.x & 127, g = warp >> 2, half = l >> 6, hl = l & 63, head = kHc * (int)rank + hl;
+    Row r;
+    for (int n0 = 0; rows.next(r); n0 += r.nblk) {
+      t_out = rows.t;
+      empty = r.nblk == 0;
+      if (r.nsel == 0 && r.klen > 0 && threadIdx.x == 0) set_status(a.status, DSA_ERR_OUT_OF_RANGE, t_out);
+      sm.m = -INFINITY;
+      sm.sum = 0.f;
+      for (int j = (n0 ^ g) & 1; j < r.nblk; j += 2) sm.block(S, a, tmem_lane, n0 + j, j, r.nblk, g, c, rank, to_first);
+      last = (n0 + r.nblk - 1) & 1;
+      // the last block's group waits for its product (to the other group's threads the
+      // barrier may still be two phases back); all meet at the barrier below
+      if (!empty && last == g) sm.dead = sm.dead || !wait_local(&S.pv_done[last], ((n0 + r.nblk - 1) >> 1) & 1, a.status, 52);
+      if (kSplits > 1) break;
+      // the row's output: the head's maximum, its sum over four threads, then this
+      // thread's half of the lane's columns
+      const bool bad = named_bar_or(1, kSmThreads, sm.dead);
       tc_fence_after();
+      const float M = empty ? -INFINITY : S.m_run[last][hl];
+      S.red[g][l] = sm.m == -INFINITY ? 0.f : sm.sum * exp2f(sm.m - M);
+      named_bar_sync(1, kSmThreads);
+      const float L = (S.red[0][hl] + S.red[1][hl]) + (S.red[0][hl + 64] + S.red[1][hl + 64]);
+      named_bar_sync(1, kSmThreads);              // read before the next row's maxima go there
+      const float inv = L > 0.f ? 1.f / L : 0.f;
+      if (empty) {
+        // the values' tiles may hold a later row's already: zeros go out directly
+        uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)t_out * a.n_heads * kDC);
+        const int from = kHc * (int)rank * (kDC / 8), to = min(a.n_heads, kHc * ((int)rank + 1)) * (kDC / 8);
+        for (int i = from + (int)threadIdx.x; i < to; i += kSmThreads) out[i] = make_uint4(0u, 0u, 0u, 0u);
+      } else {
+#pragma unroll 1
+        for (int cc = 0; cc < 4; ++cc) {
+          const int col = 128 * g + 32 * cc;
+          float o[32];
+          load_o32(tmem_lane + kColO + col, bad, o);
+          stage_bf16(smraw + Mg::kOut + (4 * half + (col >> 6)) * 8192, hl, col, o, inv);
+        }
+        tc_fence_before();
+        warp_arrive_first(&S.o_free, to_first);
+        fence_proxy_async_smem();
+        named_bar_sync(1, kSmThreads);
+        // the group that does not begin the next row sends the tiles out, those in the
+        // stage of the next block first
+        const int next = (n0 + r.nblk) & 1;
+        if (g != next && l == 0) {
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            const int tile = (4 * next) ^ i;
+            if (kHc * (int)rank < a.n_heads)
+              store_tile(&out_map, smraw + Mg::kOut + tile * 8192, 64 * tile, kHc * (int)rank, t_out);
+            if ((i & 3) == 3) bulk_commit();
+          }
+          bulk_wait_read<1>();
+          mbar_arrive(&S.v_idle[next]);
+          bulk_wait_read0();
+          mbar_arrive(&S.v_idle[next ^ 1]);
+        }
+        __syncwarp();
+      }
+      if (a.lse && half == 0 && g == 0 && head < a.n_heads)
+        a.lse[(int64_t)t_out * a.n_heads + head] = L > 0.f && !bad ? (M + log2f(L)) * kLn2 : -INFINITY;
     }
   }
 
-  // The row's output.  With key splits the pairs of the cluster first exchange what
-  // they hold, once every pair's products are done and its tiles may be overwritten.
-  using Mg = Merge<kSplits>;
-  constexpr int kCols = Mg::kCols;
+  // With key splits the pairs of the cluster exchange what they hold, once every pair's
+  // products are done and its tiles may be overwritten.
   if (kSplits > 1) {
+    constexpr int kCols = Mg::kCols;
     tc_fence_before();
     __syncthreads();
     cluster_sync();
     tc_fence_after();
-  }
-  if (warp < kSmWarps) {
-    const int l = threadIdx.x & 127, cw = threadIdx.x >> 7, half = l >> 6, hl = l & 63;
-    const uint32_t o_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColO;
-    // the head's maximum and its sum over four threads; a wait that ran out anywhere
-    // fails the CTA
-    const bool fail = named_bar_or(1, kSmThreads, sm.dead);
-    float M = empty ? -INFINITY : S.m_run[(nblk - 1) & 1][hl];
-    S.red[cw][l] = sm.m == -INFINITY ? 0.f : sm.sum * exp2f(sm.m - M);
-    named_bar_sync(1, kSmThreads);
-    float L = (S.red[0][hl] + S.red[1][hl]) + (S.red[0][hl + 64] + S.red[1][hl + 64]);
-    if (fail) L = __int_as_float(0x7FC00000);     // marks the row for the other pairs too
-    float w[kSplits];
-    w[0] = 1.f;
-    bool got = true;
-    if (kSplits > 1) {
+    if (warp < kSmWarps) {
+      const int l = threadIdx.x & 127, cw = threadIdx.x >> 7, half = l >> 6, hl = l & 63;
+      const uint32_t o_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColO;
+      // the head's maximum and its sum over four threads; a wait that ran out anywhere
+      // fails the CTA, and NaN marks the row for the other pairs too
+      const bool fail = named_bar_or(1, kSmThreads, sm.dead);
+      float M = empty ? -INFINITY : S.m_run[last][hl];
+      S.red[cw][l] = sm.m == -INFINITY ? 0.f : sm.sum * exp2f(sm.m - M);
+      named_bar_sync(1, kSmThreads);
+      float L = (S.red[0][hl] + S.red[1][hl]) + (S.red[0][hl + 64] + S.red[1][hl + 64]);
+      if (fail) L = __int_as_float(0x7FC00000);
       // parts for the other pairs, 32 columns at a time: staged, then one bulk copy
 #pragma unroll 1
       for (int cc = 0; cc < 4; ++cc) {
@@ -680,12 +886,13 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(MlaArgs a) {
       if (threadIdx.x < kSplits && threadIdx.x != sp)
         bulk_copy_to_peer(smraw + kRecvMl + sp * (size_t)Mg::kMl, ml, Mg::kMl, &S.merged, 2 * threadIdx.x + rank);
       bulk_commit();
-      got = wait_local(&S.merged, 0, a.status, 57);
+      const bool got = wait_local(&S.merged, 0, a.status, 57);
       // out = sum_s w_s O_s / sum_s w_s l_s,  w_s = 2^(m_s - max m), splits in order
+      float w[kSplits];
+      float2 v[kSplits];
       const float2 mine = make_float2(M, L);
       M = -INFINITY;
       L = 0.f;
-      float2 v[kSplits];
 #pragma unroll
       for (int s2 = 0; s2 < kSplits; ++s2) {
         v[s2] = s2 == sp ? mine : reinterpret_cast<const float2*>(smraw + kRecvMl + s2 * (size_t)Mg::kMl)[hl];
@@ -696,59 +903,52 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(MlaArgs a) {
         w[s2] = v[s2].x == -INFINITY ? 0.f : exp2f(v[s2].x - M);
         L += w[s2] * v[s2].y;                     // NaN of a failed pair stays
       }
-    }
-    const bool bad = named_bar_or(1, kSmThreads, !got) || L != L;
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    // Finished rows go through shared memory, so that each head's columns leave as
-    // two bulk copies (one from each half of the dims).
-    uint8_t* stg = smraw + Mg::kOut + (size_t)hl * Mg::kOutRow + half * 2 * kCols;
-    constexpr int kMine = kCols / 2;              // columns of this thread: 128, 64 or 32
+      const bool bad = named_bar_or(1, kSmThreads, !got) || L != L;
+      const float inv = L > 0.f ? 1.f / L : 0.f;
+      const int head = kHc * (int)rank + hl;
+      constexpr int kMine = kCols / 2;            // columns of this thread: 64 or 32
 #pragma unroll 1
-    for (int cc = 0; cc < kMine / 32; ++cc) {
-      const int col = kMine * cw + 32 * cc;       // within the pair's columns
-      float o[32];
-      load_o32(o_lane + sp * kCols + col, empty || bad, o);
-      if (kSplits > 1) {
+      for (int cc = 0; cc < kMine / 32; ++cc) {
+        const int col = kMine * cw + 32 * cc;     // within the pair's columns
         float acc[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-#pragma unroll
+#pragma unroll 1
         for (int s2 = 0; s2 < kSplits; ++s2) {
+          const float ws = s2 == 0 ? w[0] : s2 == 1 ? w[1] : s2 == 2 ? w[2 % kSplits] : w[3 % kSplits];
+          float o[32];
           if (s2 == sp) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) acc[i] = fmaf(w[s2], o[i], acc[i]);
+            load_o32(o_lane + sp * kCols + col, empty, o);
           } else {
             const uint8_t* src = smraw + (s2 < sp ? s2 : s2 - 1) * (size_t)Mg::kPart + (size_t)col * 512 + l * 16;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float4 x = *reinterpret_cast<const float4*>(src + i * 2048);
-              acc[4 * i] = fmaf(w[s2], x.x, acc[4 * i]);
-              acc[4 * i + 1] = fmaf(w[s2], x.y, acc[4 * i + 1]);
-              acc[4 * i + 2] = fmaf(w[s2], x.z, acc[4 * i + 2]);
-              acc[4 * i + 3] = fmaf(w[s2], x.w, acc[4 * i + 3]);
+              o[4 * i] = x.x, o[4 * i + 1] = x.y, o[4 * i + 2] = x.z, o[4 * i + 3] = x.w;
             }
           }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[i] = fmaf(ws, o[i], acc[i]);
         }
+        if (bad) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = bad ? 0.f : acc[i];
+          for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+        }
+        stage_bf16(smraw + Mg::kOut + (Mg::kTiles / 2 * half + (col >> 6)) * 8192, hl, sp * kCols + col, acc, inv);
       }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(stg + 2 * col + 16 * q) = pack8(&o[8 * q], inv);
+      if (a.lse && sp == 0 && cw == 0 && half == 0 && head < a.n_heads)
+        a.lse[(int64_t)t_out * a.n_heads + head] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+      fence_proxy_async_smem();
+      named_bar_sync(1, kSmThreads);
+      if (threadIdx.x < Mg::kTiles && kHc * (int)rank < a.n_heads) {
+        const int i = threadIdx.x, in_half = i % (Mg::kTiles / 2), x = 256 * (i / (Mg::kTiles / 2)) + sp * kCols + 64 * in_half;
+        store_tile(&out_map, smraw + Mg::kOut + i * 8192, x, kHc * (int)rank, t_out);
+        bulk_commit();
+      }
     }
-    fence_proxy_async_smem();
-    named_bar_sync(1, kSmThreads);
-    const int head = kHc * (int)rank + hl;
-    if (cw == 0 && head < a.n_heads) {
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((int64_t)t * a.n_heads + head) * kDC + 256 * half + sp * kCols;
-      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(out), "r"(smem_u32(stg)), "n"(2 * kCols)
-                   : "memory");
-      bulk_commit();
-      if (a.lse && sp == 0 && half == 0)
-        a.lse[(int64_t)t * a.n_heads + head] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
-    }
-    // this thread's copies are done before shared memory goes
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
+  // this thread's copies are done before shared memory goes
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   cluster_sync();                       // no access to the pair's memory is still pending
@@ -758,9 +958,20 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(MlaArgs a) {
   }
 }
 
-using Kernel = void (*)(MlaArgs);
+using Kernel = void (*)(MlaArgs, CUtensorMap);
 template <int kSplits>
 constexpr Kernel kernel_of = mla_int4_tc_kernel<kSplits>;
+
+// out [T, H, d_c] bf16, stored as tiles of 64 heads x 64 dims.
+bool make_out_map(CUtensorMap* m, const MlaArgs& a) {
+  auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (!fn) return false;
+  const cuuint64_t dim[3] = {(cuuint64_t)kDC, (cuuint64_t)a.n_heads, (cuuint64_t)a.num_rows};
+  const cuuint64_t stride[2] = {kDC * 2, (cuuint64_t)a.n_heads * kDC * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)kHc, 1}, step[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.out, dim, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 cudaLaunchConfig_t launch_config(cudaLaunchAttribute (&at)[2], int splits, int rows) {
   cudaLaunchConfig_t cfg = {};
@@ -803,6 +1014,11 @@ bool mla_int4_tc_supported(const MlaArgs& a) {
 
 dsa_status launch_mla_int4_tc(const MlaArgs& a, cudaStream_t stream) {
   if (a.num_rows == 0) return DSA_OK;
+  CUtensorMap out_map;
+  if (!make_out_map(&out_map, a)) {
+    set_error("mla_int4_tc: cuTensorMapEncodeTiled failed");
+    return DSA_ERR_CUDA;
+  }
   static std::atomic<bool> attr1[kMaxDevices] = {}, attr2[kMaxDevices] = {}, attr4[kMaxDevices] = {};
   dsa_status st;
   if ((st = set_smem_limit_once(reinterpret_cast<const void*>(kernel_of<1>), sizeof(Smem), attr1)) ||
@@ -821,12 +1037,15 @@ dsa_status launch_mla_int4_tc(const MlaArgs& a, cudaStream_t stream) {
     kernel = kernel_of<2>;
   }
   cudaLaunchAttribute at[2];
-  cudaLaunchConfig_t cfg = launch_config(at, splits, a.num_rows);
+  // without splits one resident wave of pairs shares the rows
+  int clusters = a.num_rows;
+  if (splits == 1) clusters = min(clusters, max(resident_clusters(kernel, 1), 1));
+  cudaLaunchConfig_t cfg = launch_config(at, splits, clusters);
   cfg.stream = stream;
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, out_map);
   if (e != cudaSuccess) {
     set_error("mla_int4_tc launch: %s", cudaGetErrorString(e));
     return DSA_ERR_CUDA;

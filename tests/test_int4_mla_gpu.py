@@ -336,3 +336,23 @@ def test_which_kernel_runs(N, kw, tc):
     c.algo = N.DSA_ALGO_AUTO if tc else N.DSA_ALGO_SIMT
     c.check()
     assert c.ran() & (N.DSA_KERNEL_MLA_SIMT | N.DSA_KERNEL_MLA_INT4_TC) == (N.DSA_KERNEL_MLA_INT4_TC if tc else N.DSA_KERNEL_MLA_SIMT)
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_many_rows_of_every_length(N, seed):
+    """More rows than pairs of SMs, in any order of lengths: a pair's blocks run on
+    from row to row, over empty rows and rows of one block, odd and even."""
+    rng = np.random.default_rng(seed)
+    T = [77, 150, 223, 300][seed]
+    k = rng.choice([0, 0, 1, 63, 64, 65, 128, 129, 192, 200, 256, 320, 500], T)
+    if seed == 2:
+        k[80:] = 0                                # whole pairs end in empty rows
+    if seed == 3:
+        k[:76] = 0                                # and begin with them
+    k[5] = 300
+    c = Case(N, [int(x) for x in k], topk=512, seed=seed, seqs=[int(x) for x in rng.integers(0, 9, T)]).build().call()
+    c.check(rows=[int(x) for x in np.concatenate([np.arange(0, T, 7), np.flatnonzero(k == 1)[:5], [T - 1]])])
+    assert c.status() == (0, -1)
+    first = [x.copy() for x in c.result()]
+    for x, y in zip(first, c.call().result()):
+        np.testing.assert_array_equal(x, y)

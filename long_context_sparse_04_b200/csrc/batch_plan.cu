@@ -6,15 +6,16 @@
 // include/dsa.h.
 //
 // Everything follows from four prefix sums over the requests: pages handed back,
-// pages and rows asked for (the admission), and pages and rows granted.  Every
-// CTA of the one cluster computes them for itself (a few thousand requests are a
-// few microseconds of one CTA, and a second launch or a grid-wide wait would cost
-// as much), keeps the three that the rest needs in shared memory, and writes its
-// share of the rows, table entries and pages: a binary search in shared memory
-// gives a row's request.  Lengths and the free count, which may be updated in
-// place, are written by one CTA after the cluster barrier, when every CTA has
-// read them; free-list entries read (below the old count) and written (at or
-// above it) never meet, nor do table entries read (pages held) and written.
+// pages and rows asked for (the admission), and pages and rows granted.  Every CTA
+// computes them for itself, keeps the three that the rest needs in shared memory, and
+// writes its share of the rows, table entries and pages; a binary search in shared
+// memory gives a row's request.  One CTA plans a decoding batch; a chunked prefill of
+// 131,072 rows takes 128 (redoing the sums costs them nothing: one CTA after another
+// would wait for them all the same, and a cluster, which could share them, is 8 CTAs).
+// Lengths and the free count, which may be updated in place, are written by the CTA
+// that finishes last, when every CTA has read them; free-list entries read (below the
+// old count) and written (at or above it) never meet, nor do table entries read (pages
+// held) and written.
 #include <climits>
 
 #include "dsa_kernels.cuh"
@@ -24,7 +25,6 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kMaxSeqs = 16384;        // three int32 prefix arrays in shared memory
-constexpr int kMaxCluster = 8;
 
 // One request as the rule sees it.
 struct Request {
@@ -42,11 +42,19 @@ __device__ __forceinline__ int32_t pages_of(int64_t tokens, int32_t page) {
   return (int32_t)(((uint32_t)tokens + (uint32_t)page - 1u) / (uint32_t)page);
 }
 
-__device__ __forceinline__ Request load_request(const PlanArgs& a, int b) {
+// What the caller says of a request.
+struct Lengths {
+  int32_t len, add, rel;
+};
+__device__ __forceinline__ Lengths load_lengths(const PlanArgs& a, int b) {
+  return Lengths{a.p.seq_len[b], a.p.n_new[b], a.p.release != nullptr ? a.p.release[b] : 0};
+}
+
+__device__ __forceinline__ Request request_of(const PlanArgs& a, int b, const Lengths& x) {
   Request r;
-  r.len = a.p.seq_len[b];
-  r.add = a.p.n_new[b];
-  r.rel = a.p.release != nullptr && a.p.release[b] != 0;
+  r.len = x.len;
+  r.add = x.add;
+  r.rel = x.rel != 0;
   r.held = r.need = r.give = 0;
   r.err = 0;
   const int64_t width = a.block_table ? (int64_t)a.max_pages_per_seq * a.page_size
@@ -106,18 +114,26 @@ __device__ __forceinline__ int owner(const int32_t* start, int n, int32_t i) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) batch_plan_kernel(const PlanArgs a) {
+// What the CTAs share in the workspace's status block, zero between calls: CTAs that
+// are done, and INT_MAX - (8 * request + error) of the lowest request in error.
+struct PlanShared {
+  unsigned int done;
+  int worst;
+};
+static_assert(sizeof(PlanShared) <= sizeof(DeviceStatus::pad), "status block");
+
+__global__ void __launch_bounds__(kThreads, 1) batch_plan_kernel(const __grid_constant__ PlanArgs a) {
   extern __shared__ int32_t sm[];
   __shared__ int64_t part[2][kThreads / 32];
-  __shared__ int s_err, s_refused;
+  __shared__ int s_worst, s_refused, s_last;
   const int B = a.num_seqs, tid = threadIdx.x;
   int32_t* tok_start = sm;                  // rows granted before request b, [B + 1]
   int32_t* pg_start = sm + (B + 1);         // pages granted
   int32_t* give_start = sm + 2 * (B + 1);   // pages handed back
-  const uint32_t rank = cluster_ctarank(), nranks = cluster_nctarank();
+  PlanShared* shared = reinterpret_cast<PlanShared*>(a.status->pad);
   pdl_launch_dependents();
   trace_kernel(a.status, DSA_KERNEL_BATCH_PLAN);
-  if (tid == 0) { s_err = INT_MAX; s_refused = 0; }
+  if (tid == 0) { s_worst = 0; s_refused = 0; }
 
   int64_t F = 0;
   bool bad_count = false;
@@ -128,47 +144,53 @@ __global__ void __launch_bounds__(kThreads, 1) batch_plan_kernel(const PlanArgs 
   }
   __syncthreads();
 
-  cluster_arrive();                         // s_err is initialised (waited for below)
-
-  // thread i owns the requests [i * per, i * per + per)
+  // thread i owns the requests [i * per, i * per + per); the three arrays first hold
+  // what each request asks for or hands back
   const int per = (B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
-  // pages handed back
-  int64_t give = 0, zero = 0, gives = 0, unused = 0;
-  for (int b = b0; b < b1; ++b) {
-    const Request r = load_request(a, b);
-    give += r.give;
-    if (r.err) atomicMin(&s_err, b * 8 + r.err);
+  int64_t give = 0, rows = 0, need = 0, zero = 0, gives, ignore0, ignore1;
+  int refused = 0;
+  constexpr int kBatch = 4;                 // loads of as many requests at a time
+  for (int bb = b0; bb < b1; bb += kBatch) {
+    Lengths x[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (bb + i < b1) x[i] = load_lengths(a, bb + i);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int b = bb + i;
+      if (b >= b1) break;
+      const Request r = request_of(a, b, x[i]);
+      tok_start[b] = (int32_t)r.rows();
+      pg_start[b] = r.need;
+      give_start[b] = r.give;
+      rows += r.rows();
+      need += r.need;
+      give += r.give;
+      if (r.err) {
+        atomicMax(&s_worst, INT_MAX - (b * 8 + r.err));
+        ++refused;
+      }
+    }
   }
-  block_scan2(give, zero, gives, unused, part);
-  for (int b = b0; b < b1; ++b) {
-    give_start[b] = (int32_t)give;
-    give += load_request(a, b).give;
-  }
+  block_scan2(give, zero, gives, ignore0, part);
+  block_scan2(need, rows, ignore0, ignore1, part);
   const int64_t have = F + gives;
   // the admission: inclusive sums of pages and rows over every request that could run
-  int64_t need = 0, rows = 0;
-  for (int b = b0; b < b1; ++b) {
-    const Request r = load_request(a, b);
-    need += r.need;
-    rows += r.rows();
-  }
-  int64_t ignore0, ignore1;
-  block_scan2(need, rows, ignore0, ignore1, part);
   int64_t my_rows = 0, my_pages = 0;
-  int refused = 0;
   for (int b = b0; b < b1; ++b) {
-    const Request r = load_request(a, b);
-    need += r.need;
-    rows += r.rows();
-    const bool go = r.err == 0 && !r.rel && (r.need == 0 || need <= have) &&
-                    (r.add == 0 || rows <= a.p.max_tokens);
-    // granted rows and pages of b, kept in place of their sums for now
-    tok_start[b] = go ? (int32_t)r.add : 0;
-    pg_start[b] = go ? r.need : 0;
-    my_rows += tok_start[b];
-    my_pages += pg_start[b];
-    refused += !go && (r.err == DSA_ERR_INVALID_ARG || (!r.rel && r.add > 0));
+    const int32_t n = tok_start[b], p = pg_start[b], g = give_start[b];
+    need += p;
+    rows += n;
+    const bool go = (p == 0 || need <= have) && (n == 0 || rows <= a.p.max_tokens);
+    if (!go) {
+      tok_start[b] = pg_start[b] = 0;
+      ++refused;
+    }
+    my_rows += go ? n : 0;
+    my_pages += go ? p : 0;
+    give_start[b] = (int32_t)give;
+    give += g;
   }
   if (refused) atomicAdd(&s_refused, refused);
   int64_t total, taken;
@@ -199,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) batch_plan_kernel(const PlanArgs 
     const int32_t pg = i < F ? a.p.free_pages[i] : handed_back((int32_t)(i - F));
     return pg >= 0 && pg < a.num_pages ? pg : -1;
   };
-  const int gid = (int)rank * kThreads + tid, step = (int)nranks * kThreads;
+  const int gid = blockIdx.x * kThreads + tid, step = gridDim.x * kThreads;
   const int32_t n_rows = (int32_t)total;
   const int last = n_rows > 0 ? owner(tok_start, B, n_rows - 1) : 0;
   for (int64_t t64 = gid; t64 < a.p.max_tokens; t64 += step) {
@@ -215,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) batch_plan_kernel(const PlanArgs 
         const int32_t pg = pos / a.page_size, held = pages_of(len, a.page_size);
         int32_t page = pg >= held ? taken_page(pg_start[b] + pg - held) : a.block_table[(int64_t)b * W + pg];
         if (page < 0 || page >= a.num_pages) {
-          atomicMin(&s_err, b * 8 + DSA_ERR_OUT_OF_RANGE);
+          atomicMax(&s_worst, INT_MAX - (b * 8 + DSA_ERR_OUT_OF_RANGE));
           page = -1;
         }
         if (page >= 0) slot = (int64_t)page * a.page_size + (pos - pg * a.page_size);
@@ -237,21 +259,27 @@ __global__ void __launch_bounds__(kThreads, 1) batch_plan_kernel(const PlanArgs 
   for (int64_t i = F + gid; i < left; i += step) a.p.free_pages[i] = handed_back((int32_t)(i - F));
   for (int b = gid; b <= B; b += step) a.p.tok_start[b] = tok_start[b];
 
-  // the lowest request in error, over the cluster
-  cluster_wait();
+  // the CTA that is done last has the rest: every CTA has read the lengths and the free
+  // count, and said what it found wrong
   __syncthreads();
-  if (rank != 0 && tid == 0 && s_err != INT_MAX)
-    asm volatile("red.relaxed.cluster.shared::cluster.min.s32 [%0], %1;" ::"r"(mapa(&s_err, 0)), "r"(s_err)
-                 : "memory");
-  cluster_sync();                           // every CTA has read the lengths and the free count
-  if (rank != 0) return;
-  if (tid == 0 && s_err != INT_MAX) set_status(a.status, s_err & 7, s_err >> 3);
+  if (tid == 0) {
+    if (s_worst) atomicMax(&shared->worst, s_worst);
+    __threadfence();
+    s_last = gridDim.x == 1 || atomicAdd(&shared->done, 1u) == gridDim.x - 1;
+    __threadfence();
+  }
+  __syncthreads();
+  if (!s_last) return;
   for (int b = tid; b < B; b += kThreads) {
-    const Request r = load_request(a, b);
+    const Request r = request_of(a, b, load_lengths(a, b));
     const int32_t n = tok_start[b + 1] - tok_start[b];
     a.p.seq_len_out[b] = r.rel && r.err == 0 ? 0 : (int32_t)(r.len + n);
   }
   if (tid == 0) {
+    const int worst = *reinterpret_cast<volatile int*>(&shared->worst);
+    if (worst) set_status(a.status, (INT_MAX - worst) & 7, (INT_MAX - worst) >> 3);
+    shared->worst = 0;
+    shared->done = 0;
     if (bad_count || have - taken > left) set_status(a.status, DSA_ERR_INVALID_ARG, -1);
     if (a.block_table) *a.p.free_count_out = (int32_t)left;
     a.p.totals[0] = n_rows;
@@ -270,21 +298,11 @@ dsa_status launch_batch_plan(const PlanArgs& a, cudaStream_t stream) {
   static std::atomic<bool> attr[kMaxDevices] = {};
   if (dsa_status st = set_smem_limit_once(reinterpret_cast<const void*>(batch_plan_kernel), smem_max, attr))
     return st;
-  int ctas = 1;
-  while (ctas < kMaxCluster && (int64_t)ctas * kThreads < a.p.max_tokens) ctas <<= 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)3 * (a.num_seqs + 1) * sizeof(int32_t);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)ctas;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, batch_plan_kernel, a);
+  // a CTA for every kThreads rows, at most one per SM
+  const int64_t want = ((int64_t)a.p.max_tokens + kThreads - 1) / kThreads;
+  const int most = device_sm_count(), ctas = want < 1 ? 1 : want < most ? (int)want : most;
+  batch_plan_kernel<<<ctas, kThreads, (size_t)3 * (a.num_seqs + 1) * sizeof(int32_t), stream>>>(a);
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("batch plan launch failed: %s", cudaGetErrorString(e));
     return DSA_ERR_CUDA;

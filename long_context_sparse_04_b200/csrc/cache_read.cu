@@ -31,49 +31,84 @@ __device__ __forceinline__ float4 e4m3x4_to_f32(uint32_t w, float s) {
   return make_float4(f[0], f[1], f[2], f[3]);
 }
 
-template <bool kInt4>
-__global__ void __launch_bounds__(kWarpsPerCta * 32) cache_read_kernel(const ReadArgs a) {
+// Streaming stores: the output is not read again here.
+__device__ __forceinline__ void st_stream(uint4* p, const uint4& v) { __stcs(p, v); }
+
+__device__ __forceinline__ int64_t slot_of(const ReadArgs& a, int64_t n) {
+  if (n >= a.n) return -1;
+  const int64_t row = __ldg(reinterpret_cast<const long long*>(a.slot) + n);
+  if (row < a.num_tokens) return row;
+  if ((threadIdx.x & 31) == 0) set_status(a.status, DSA_ERR_OUT_OF_RANGE, (int)n);
+  return -1;
+}
+
+// Packed rows, one warp per token.  A lane decodes words of eight dims, 32 apart, so
+// that a warp's stores are whole lines, and all of a token's loads are issued before
+// its first store (d_c <= 512: two words a lane).
+__global__ void __launch_bounds__(kWarpsPerCta * 32) cache_read_int4_kernel(const __grid_constant__ ReadArgs a) {
   pdl_launch_dependents();
   trace_kernel(a.status, DSA_KERNEL_CACHE_READ);
   const int lane = threadIdx.x & 31;
-  const int n = blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
-  if (n >= a.n) return;
-  const int64_t row = a.slot[n];
+  const int64_t n = (int64_t)blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5), row = slot_of(a, n);
   if (row < 0) return;
-  if (row >= a.num_tokens) {
-    if (lane == 0) set_status(a.status, DSA_ERR_OUT_OF_RANGE, n);
-    return;
-  }
-  if (a.k_out != nullptr) {
-    float4* dst = reinterpret_cast<float4*>(a.k_out + (int64_t)n * a.d_idx);
-    const int chunks = a.d_idx >> 2;
-    if (a.idx_dtype == DSA_FP8_E4M3) {
-      const float s = a.idx_k_scale[row];
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.idx_k) + row * a.d_idx);
-      for (int c = lane; c < chunks; c += 32) dst[c] = e4m3x4_to_f32(src[c], s);
-    } else {
-      const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.idx_k) + row * a.d_idx);
-      for (int c = lane; c < chunks; c += 32) dst[c] = src[c];
+  const Int4Row ly = int4_row(a.d_c, a.d_r);
+  const uint8_t* src = static_cast<const uint8_t*>(a.latent) + row * ly.bytes;
+  const bool lat = a.latent_out != nullptr, fp8 = a.idx_dtype == DSA_FP8_E4M3;
+  const int words = lat ? a.d_c >> 3 : 0, pieces = lat ? a.d_r >> 3 : 0, keys = a.k_out != nullptr ? a.d_idx >> 2 : 0;
+  uint32_t code[2], scale[2], key = 0;
+  float ks = 0.f;
+  uint4 rope;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int w = lane + 32 * i;
+    if (w < words) {
+      code[i] = __ldg(reinterpret_cast<const uint32_t*>(src) + w);
+      scale[i] = __ldg(src + ly.scale + (w >> 1));
     }
   }
-  if (a.latent_out == nullptr) return;
-  const uint8_t* src = static_cast<const uint8_t*>(a.latent) + row * a.latent_row_bytes;
-  if constexpr (kInt4) {
-    const Int4Row ly = int4_row(a.d_c, a.d_r);
-    const int groups = a.d_c / kInt4Group, pieces = a.d_r >> 3;
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.latent_out) + (int64_t)n * (a.d_c + a.d_r));
-    for (int g = lane; g < groups; g += 32) {
-      const uint2 w = reinterpret_cast<const uint2*>(src)[g];
-      const ScalePair s = scale_pair(src[ly.scale + g]);
-      dst[2 * g] = decode_word(w.x, s);
-      dst[2 * g + 1] = decode_word(w.y, s);
-    }
-    for (int c = lane; c < pieces; c += 32)
-      dst[2 * groups + c] = reinterpret_cast<const uint4*>(src + ly.rope)[c];
+  if (lane < pieces) rope = __ldg(reinterpret_cast<const uint4*>(src + ly.rope) + lane);
+  const uint32_t* kw = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.idx_k) + row * a.d_idx);
+  if (fp8 && lane < keys) {
+    key = __ldg(kw + lane);
+    ks = __ldg(a.idx_k_scale + row);
+  }
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.latent_out) + n * (a.d_c + a.d_r));
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (lane + 32 * i < words) st_stream(dst + lane + 32 * i, decode_word(code[i], scale_pair(scale[i])));
+  if (lane < pieces) st_stream(dst + words + lane, rope);
+  for (int c = lane + 32; c < pieces; c += 32) st_stream(dst + words + c, __ldg(reinterpret_cast<const uint4*>(src + ly.rope) + c));
+  float4* kdst = reinterpret_cast<float4*>(a.k_out + n * a.d_idx);
+  if (fp8) {
+    if (lane < keys) __stcs(kdst + lane, e4m3x4_to_f32(key, ks));
+    for (int c = lane + 32; c < keys; c += 32) __stcs(kdst + c, e4m3x4_to_f32(__ldg(kw + c), ks));
   } else {
-    const int pieces = a.latent_row_bytes >> 4;
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.latent_out) + (int64_t)n * a.latent_row_bytes);
-    for (int c = lane; c < pieces; c += 32) dst[c] = reinterpret_cast<const uint4*>(src)[c];
+    const float4* kf = reinterpret_cast<const float4*>(static_cast<const float*>(a.idx_k) + row * a.d_idx);
+    for (int c = lane; c < keys; c += 32) __stcs(kdst + c, __ldg(kf + c));
+  }
+}
+
+// Caches of the values' own type: a copy of the latent row, the key as above.
+__global__ void __launch_bounds__(kWarpsPerCta * 32) cache_read_kernel(const __grid_constant__ ReadArgs a) {
+  pdl_launch_dependents();
+  trace_kernel(a.status, DSA_KERNEL_CACHE_READ);
+  const int lane = threadIdx.x & 31;
+  const int64_t n = (int64_t)blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5), row = slot_of(a, n);
+  if (row < 0) return;
+  const int words = a.k_out != nullptr ? a.d_idx >> 2 : 0;
+  const int pieces = a.latent_out != nullptr ? a.latent_row_bytes >> 4 : 0;
+  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.latent) + row * a.latent_row_bytes);
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.latent_out) + n * a.latent_row_bytes);
+#pragma unroll 4
+  for (int c = lane; c < pieces; c += 32) st_stream(dst + c, __ldg(src + c));
+  if (a.idx_dtype == DSA_FP8_E4M3) {
+    const uint32_t* key = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.idx_k) + row * a.d_idx);
+    const float s = words > 0 ? __ldg(a.idx_k_scale + row) : 0.f;
+    for (int c = lane; c < words; c += 32)
+      __stcs(reinterpret_cast<float4*>(a.k_out + n * a.d_idx) + c, e4m3x4_to_f32(__ldg(key + c), s));
+  } else {
+    const float4* key = reinterpret_cast<const float4*>(static_cast<const float*>(a.idx_k) + row * a.d_idx);
+    for (int c = lane; c < words; c += 32) __stcs(reinterpret_cast<float4*>(a.k_out + n * a.d_idx) + c, __ldg(key + c));
   }
 }
 
@@ -82,7 +117,7 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) cache_read_kernel(const Rea
 dsa_status launch_cache_read(const ReadArgs& a, cudaStream_t stream) {
   if (a.n == 0) return DSA_OK;
   const unsigned grid = (unsigned)(((int64_t)a.n + kWarpsPerCta - 1) / kWarpsPerCta);
-  (a.int4 ? cache_read_kernel<true> : cache_read_kernel<false>)<<<grid, kWarpsPerCta * 32, 0, stream>>>(a);
+  (a.int4 ? cache_read_int4_kernel : cache_read_kernel)<<<grid, kWarpsPerCta * 32, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("cache read launch failed: %s", cudaGetErrorString(e));

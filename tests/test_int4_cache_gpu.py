@@ -146,6 +146,52 @@ def test_append_by_slot_then_read(N, n, d_c, d_r, d_idx, fp8):
     assert N.dsa_read_kernel_trace(c.ws.data_ptr(), c.args()[2]) == N.DSA_KERNEL_CACHE_APPEND | N.DSA_KERNEL_CACHE_READ
 
 
+def test_every_scale_and_tie(N):
+    """Every finite bf16 as a group's largest value, with every tie of its scale."""
+    amax = R.bf16_decode(np.arange(1, 0x7F80, dtype=np.uint16)).astype(np.float64)
+    s = R.int4_scale_decode(R.int4_scale_encode((amax.astype(np.float32) / np.float32(7))))
+    g = np.zeros((len(amax), 16))
+    g[:, 0] = amax * np.where(np.arange(len(amax)) % 2, 1, -1)
+    for j in range(7):                                         # (j + 1/2) scale: exact in bf16, below amax or clipped to it
+        g[:, 1 + j] = np.minimum((j + 0.5) * s, amax)
+        g[:, 8 + j] = -np.minimum(np.nextafter(np.float32(1), np.float32(2)) * (j + 0.5) * s * (1 + 2.0 ** -7), amax)
+    g[:, 15] = np.minimum(s * 0.25, amax)
+    rows = -(-len(amax) // 32)
+    lat = np.zeros((rows, 512), np.float32)
+    lat.reshape(-1)[: g.size] = g.reshape(-1)
+    bits = I.to_bf16_bits(lat)
+    d = dims(N, 512, 0, 4)
+    c = Cache(N, d, rows)
+    N.dsa_cache_append_slots(d, c.c, rows, dev(np.arange(rows, dtype=np.int64)).data_ptr(), None, dev(bits).data_ptr(), *c.args())
+    np.testing.assert_array_equal(c.bytes()[0], R.int4_pack(bits, 512, 0))
+    assert c.status() == (0, -1)
+
+
+def test_keys_at_the_borders_of_e4m3(N):
+    """Keys whose quotient lies on, or a unit in the last place beside, every border
+    between two e4m3 codes, under scales of many magnitudes."""
+    rng = np.random.default_rng(2)
+    vals = np.unique(np.abs(R.e4m3_decode(np.arange(127, dtype=np.uint8)))).astype(np.float64)
+    mids = (vals[1:] + vals[:-1]) / 2
+    scales = np.exp(rng.uniform(-80, 80, 300)).astype(np.float32)
+    scales[:4] = [1e-40, 1.0, 3e-39, 2.0 ** -149 * 3]
+    k = np.zeros((len(scales), 508), np.float32)
+    for r, s in enumerate(scales):
+        m = (mids * np.float64(s)).astype(np.float32)
+        row = np.concatenate([m, np.nextafter(m, np.float32(np.inf)), np.nextafter(m, np.float32(0)), -m])
+        k[r, : len(row)] = row
+        k[r, -1] = np.float32(448) * s
+    k = np.where(np.isfinite(k), k, 0).astype(np.float32)
+    d = dims(N, 32, 0, 508)
+    c = Cache(N, d, len(scales))
+    N.dsa_cache_append_slots(d, c.c, len(scales), dev(np.arange(len(scales), dtype=np.int64)).data_ptr(), dev(k).data_ptr(),
+                             None, *c.args())
+    codes, s = R.quantise_keys(k)
+    got = c.bytes()
+    np.testing.assert_array_equal(got[1], codes)
+    np.testing.assert_array_equal(got[2], s)
+
+
 def test_every_byte_reads_as_its_value(N):
     """All 16 codes at all 256 scale bytes, those the writers never use among them."""
     import torch

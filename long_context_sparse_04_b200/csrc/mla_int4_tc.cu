@@ -101,14 +101,15 @@ static_assert(offsetof(Smem, k) % 1024 == 0 && offsetof(Smem, v) % 1024 == 0 && 
 // The merge of a row's key splits S: pair s finishes columns [256 s / S, 256 (s + 1) / S)
 // of every lane and gets them from the other pairs, [source][column / 4][lane] float4,
 // where Q lay, with (max, sum) per source and head; it sends its other columns from
-// behind that.  Finished columns are staged as tiles of 64 heads x 64 dims (128-byte
+// behind that.  Copies between CTAs run at 16 bytes a cycle, 2 us of a row of two splits
+// and 128 heads, so only the lanes of heads that exist travel.  Finished columns are staged as tiles of 64 heads x 64 dims (128-byte
 // rows, swizzled), one bulk tensor store each: in the values' tiles, idle between a
 // row's last product and the next row's first, or with splits behind what is sent.
 constexpr size_t kRecvMl = 3 * 32768, kSendMl = kRecvMl + kMaxPairs * kHc * 8, kSend = kRecvMl + 4096;
 template <int kSplits>
 struct Merge {
   static constexpr int kCols = 256 / kSplits;                   // columns of a lane that a pair finishes
-  static constexpr uint32_t kPart = kCols * 512, kMl = kHc * 8; // bytes of one source's part
+  static constexpr uint32_t kPart = kCols * 512, kMl = kHc * 8; // bytes of one source's part, at most
   static constexpr int kTiles = 8 / kSplits;                    // staged tiles: kTiles / 2 from each half of the dims
   static constexpr size_t kOut =
       kSplits == 1 ? offsetof(Smem, v) : (kSend + (kSplits - 1) * (size_t)kPart + 1023) / 1024 * 1024;
@@ -185,6 +186,10 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, 
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+// cluster_arrive() that orders no memory accesses.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 // True in one lane of a converged warp.  The compiler knows that what follows is
 // run by one thread and keeps the descriptors in uniform registers; under
@@ -303,10 +308,11 @@ __device__ __forceinline__ void issue_products(Smem& S, RowStream<kSplits> rows,
       }
     }
   }
-  // every product issued is done before the pair's shared and tensor memory go
+  // the last row's arrivals from the other CTA are in, and every product issued is done,
+  // before the pair's shared and tensor memory go
+  if (kSplits == 1 && ok && busy > 0) wait_local(&S.o_free, (busy - 1) & 1, status, 58);
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&S.drained))
                : "memory");
-  wait_local(&S.drained, 0, status, 46);
 }
 
 // ---------------------------------------------------------------- the selection
@@ -323,6 +329,15 @@ __device__ __forceinline__ void resolve_rows(Smem& S, RowStream<kSplits> rows, u
     int seq;
     bool any;                                     // a block at all
   };
+  // The first block's positions, where a full selection has them, go to L1 while the
+  // row's length is on its way.
+  const int guess = (a.topk + kSplits * kBlk - 1) / (kSplits * kBlk) * kBlk * rows.sp + lane;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    int32_t unused;
+    if (guess + 32 * u < a.topk)
+      asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(unused) : "l"(a.idx + (int64_t)(rows.t + rows.step) * a.topk + guess + 32 * u));
+  }
   Row r;
   r.nblk = 0;
   int j = 0;
@@ -502,20 +517,22 @@ __device__ __forceinline__ void decode_blocks(Smem& S, RowStream<kSplits> rows, 
     while (known <= n && ahead.next_busy(x)) known += x.nblk;
     return n < known;
   };
-  bool ok = true;
-  Row r;
-  if (comes(0)) load_q(ahead.t);                  // the first row's, while its selection is resolved
-  if (comes(g)) {
-    ok = load_keys(g);
-    load_values();
-  }
   const auto q_landed = [&] {
     cp_async_wait_all();
     fence_proxy_async_smem();
     warp_arrive_first(&S.q_full, first);
   };
+  bool ok = true;
+  Row r;
+  // the first row's Q, while its selection is resolved (and done with before the first
+  // tile's loads, for which the fence would wait)
+  if (comes(0)) load_q(ahead.t);
   cluster_wait();                                 // the first CTA's barriers are initialised
   if (known > 0) q_landed();
+  if (comes(g)) {
+    ok = load_keys(g);
+    load_values();
+  }
   uint32_t busy = 0;                              // rows with keys so far
   for (int n0 = 0; ok && rows.next_busy(r); n0 += r.nblk, ++busy) {
     bool q_pending = n0 > 0, first_in_row = true;
@@ -565,14 +582,16 @@ __device__ __forceinline__ void decode_blocks(Smem& S, RowStream<kSplits> rows, 
   cp_async_wait_all();                            // after a wait that ran out
 }
 
-// 32 columns of this thread's lane of O (zeros when no product was issued).
-__device__ __forceinline__ void load_o32(uint32_t taddr, bool empty, float (&o)[32]) {
+// N columns of this thread's lane of O (zeros when no product was issued).
+template <int N>
+__device__ __forceinline__ void load_o(uint32_t taddr, bool empty, float (&o)[N]) {
   if (empty) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] = 0.f;
+    for (int i = 0; i < N; ++i) o[i] = 0.f;
     return;
   }
-  tmem_ld32(taddr, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
+  if constexpr (N == 32) tmem_ld32(taddr, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
+  else tmem_ld16(taddr, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
   tmem_wait_ld();
 }
 
@@ -701,11 +720,12 @@ struct Softmax {
   }
 };
 
-// 32 columns (from `col`, of a lane's 256) of head hl, scaled and rounded, into the
+// N columns (from `col`, of a lane's 256) of head hl, scaled and rounded, into the
 // 128-byte row of its staged tile, the values' permutation undone.
-__device__ __forceinline__ void stage_bf16(uint8_t* tile, int hl, int col, const float (&o)[32], float scale) {
+template <int N>
+__device__ __forceinline__ void stage_bf16(uint8_t* tile, int hl, int col, const float (&o)[N], float scale) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
+  for (int q = 0; q < N / 8; ++q)
     *reinterpret_cast<uint4*>(tile + sw128_off(hl, value_piece(col >> 6, (col >> 3 & 7) + q))) = pack8(&o[8 * q], scale);
 }
 // A staged tile to dims [x, x + 64) of heads [y, y + 64) of row t (heads beyond H are
@@ -725,6 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_c
   const uint32_t crank = cluster_ctarank(), rank = crank & 1u, first = crank & ~1u;
   const int sp = (int)(crank >> 1);
   const uint32_t to_first = mapa(smraw, first) - smem_u32(smraw);
+  const int heads = max(0, min(kHc, a.n_heads - kHc * (int)rank));  // of this CTA
   pdl_launch_dependents();
 
   if (threadIdx.x == 0) {
@@ -745,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_c
     }
     mbar_init(&S.merged, 1);
     fence_mbar_init();
-    if (kSplits > 1) mbar_expect_tx(&S.merged, (kSplits - 1) * (Merge<kSplits>::kPart + Merge<kSplits>::kMl));
+    if (kSplits > 1) mbar_expect_tx(&S.merged, (kSplits - 1) * (Merge<kSplits>::kCols * 8 * heads + Merge<kSplits>::kMl));
   }
   __syncwarp();
   if (warp == kMmaWarp) tmem_alloc_pair(&S.tmem_base, kTmemCols);
@@ -758,46 +779,53 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_c
   trace_kernel(a.status, kSplits > 1 ? DSA_KERNEL_MLA_INT4_TC | DSA_KERNEL_MLA_COMBINE : DSA_KERNEL_MLA_INT4_TC);
   // with splits one row per cluster, else the pair's share of the rows
   RowStream<kSplits> rows(a, blockIdx.x / (2 * kSplits), kSplits > 1 ? a.num_rows : (int)gridDim.x / 2, sp);
-  // what the output needs of the last row (with splits: of the only one)
   using Mg = Merge<kSplits>;
-  Softmax sm;
-  bool empty = true;
-  int last = 0, t_out = 0;
 
   if (warp == kMmaWarp) {
     cluster_wait();
     if (rank == 0 && elect_one()) issue_products<kSplits>(S, rows, tmem, (uint16_t)(3u << first));
     __syncwarp();
+    cluster_arrive();
+    if (rank == 0) wait_warp(&S.drained, 0, a.status, 46);
   } else if (warp == kRowWarp) {
     resolve_rows<kSplits>(S, rows, rank);
     cluster_wait();
+    cluster_arrive();
   } else if (warp >= kDecWarp0) {
     const int w = warp - kDecWarp0;
     decode_blocks<kSplits>(S, rows, rank, to_first, w % kDecWarps, w / kDecWarps);
+    cluster_arrive();
   } else {
     cluster_wait();
     const float c = a.sm_scale * kLog2e;
     const uint32_t tmem_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const int l = threadIdx.x & 127, g = warp >> 2, half = l >> 6, hl = l & 63, head = kHc * (int)rank + hl;
+    Softmax sm;
     Row r;
+    bool settled = true;                          // no wait ran out in either group
     for (int n0 = 0; rows.next(r); n0 += r.nblk) {
-      t_out = rows.t;
-      empty = r.nblk == 0;
+      const int t_out = rows.t, last = (n0 + r.nblk - 1) & 1;
+      const bool empty = r.nblk == 0;
       if (r.nsel == 0 && r.klen > 0 && threadIdx.x == 0) set_status(a.status, DSA_ERR_OUT_OF_RANGE, t_out);
       sm.m = -INFINITY;
       sm.sum = 0.f;
       for (int j = (n0 ^ g) & 1; j < r.nblk; j += 2) sm.block(S, a, tmem_lane, n0 + j, j, r.nblk, g, c, rank, to_first);
-      last = (n0 + r.nblk - 1) & 1;
+      if (kSplits > 1) cluster_arrive();
       // the last block's group waits for its product (to the other group's threads the
       // barrier may still be two phases back); all meet at the barrier below
       if (!empty && last == g) sm.dead = sm.dead || !wait_local(&S.pv_done[last], ((n0 + r.nblk - 1) >> 1) & 1, a.status, 52);
-      if (kSplits > 1) break;
       // the row's output: the head's maximum, its sum over four threads, then this
       // thread's half of the lane's columns
       const bool bad = named_bar_or(1, kSmThreads, sm.dead);
+      settled = settled && !bad;
       tc_fence_after();
       const float M = empty ? -INFINITY : S.m_run[last][hl];
       S.red[g][l] = sm.m == -INFINITY ? 0.f : sm.sum * exp2f(sm.m - M);
+      if (kSplits > 1) {
+        // NaN marks the row for whoever takes part in the merge, in the other pairs too
+        if (bad) S.red[g][l] = __int_as_float(0x7FC00000);
+        break;
+      }
       named_bar_sync(1, kSmThreads);
       const float L = (S.red[0][hl] + S.red[1][hl]) + (S.red[0][hl + 64] + S.red[1][hl + 64]);
       named_bar_sync(1, kSmThreads);              // read before the next row's maxima go there
@@ -812,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_c
         for (int cc = 0; cc < 4; ++cc) {
           const int col = 128 * g + 32 * cc;
           float o[32];
-          load_o32(tmem_lane + kColO + col, bad, o);
+          load_o(tmem_lane + kColO + col, bad, o);
           stage_bf16(smraw + Mg::kOut + (4 * half + (col >> 6)) * 8192, hl, col, o, inv);
         }
         tc_fence_before();
@@ -840,118 +868,132 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_c
       if (a.lse && half == 0 && g == 0 && head < a.n_heads)
         a.lse[(int64_t)t_out * a.n_heads + head] = L > 0.f && !bad ? (M + log2f(L)) * kLn2 : -INFINITY;
     }
+    if (kSplits == 1) {
+      // A release would wait for the output's stores as well (1,500 cycles).  There is no
+      // need of one when what this warp sent to the other CTA has led to the products and
+      // the end of the issue, o_free, that were waited for.
+      bulk_wait_read0();                          // what this thread's copies read may go
+      tc_fence_before();
+      __syncwarp();
+      if (settled) cluster_arrive_relaxed();
+      else cluster_arrive();
+    }
   }
 
-  // With key splits the pairs of the cluster exchange what they hold, once every pair's
-  // products are done and its tiles may be overwritten.
-  if (kSplits > 1) {
-    constexpr int kCols = Mg::kCols;
+  // With key splits the pairs of the cluster exchange what they hold, all of a CTA's
+  // warps taking part (four read a column of tensor memory, so in groups of four).
+  if constexpr (kSplits > 1) {
+    constexpr int kCols = Mg::kCols, kItems = (kSplits - 1) * kCols / 32;
+    static_assert(kItems <= kDecWarp0 / 4 + 2 * kDecWarps / 4, "a group sends 32 columns at most");
     tc_fence_before();
     __syncthreads();
-    cluster_sync();
     tc_fence_after();
-    if (warp < kSmWarps) {
-      const int l = threadIdx.x & 127, cw = threadIdx.x >> 7, half = l >> 6, hl = l & 63;
+    // A CTA's threads arrived when its last S was done, or with its last weights: Q's and
+    // the keys' tiles, where the parts arrive, are free then, and the barrier is complete
+    // by the time that the last product is.  Parts are sent from where the values lay.
+    cluster_wait();
+    if (warp < kMmaWarp) {
+      const int l = threadIdx.x & 127, grp = warp >> 2, half = l >> 6, hl = l & 63;
       const uint32_t o_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColO;
-      // the head's maximum and its sum over four threads; a wait that ran out anywhere
-      // fails the CTA, and NaN marks the row for the other pairs too
-      const bool fail = named_bar_or(1, kSmThreads, sm.dead);
-      float M = empty ? -INFINITY : S.m_run[last][hl];
-      S.red[cw][l] = sm.m == -INFINITY ? 0.f : sm.sum * exp2f(sm.m - M);
-      named_bar_sync(1, kSmThreads);
+      const Row r = row_of<kSplits>(a, rows.klen_next, rows.seq_next, sp);
+      const int t = blockIdx.x / (2 * kSplits);
+      const bool none = r.nblk == 0;
+      float M = none ? -INFINITY : S.m_run[(r.nblk - 1) & 1][hl];
       float L = (S.red[0][hl] + S.red[1][hl]) + (S.red[0][hl + 64] + S.red[1][hl + 64]);
-      if (fail) L = __int_as_float(0x7FC00000);
-      // parts for the other pairs, 32 columns at a time: staged, then one bulk copy
-#pragma unroll 1
-      for (int cc = 0; cc < 4; ++cc) {
-        const int col = 128 * cw + 32 * cc, to = col / kCols;
-        if (to == sp) continue;
+      const bool fail = __any_sync(0xffffffffu, L != L);
+      // a column group's 16 bytes of every lane that travels; this lane's place there
+      const uint32_t lanes16 = 32u * heads, lane16 = 16u * (half * heads + hl);
+      if (grp < kItems) {
+        const int dst = grp * 32 / kCols, to = dst < sp ? dst : dst + 1, in_slot = sp < to ? sp : sp - 1;
+        const int col = grp * 32 % kCols;
         float o[32];
-        load_o32(o_lane + col, empty || fail, o);
-        const int out_slot = to < sp ? to : to - 1, in_slot = sp < to ? sp : sp - 1;
-        const size_t off = (size_t)(col - to * kCols) * 512;
-        uint8_t* src = smraw + kSend + out_slot * (size_t)Mg::kPart + off;
+        load_o(o_lane + to * kCols + col, none || fail, o);
+        uint8_t* src = smraw + kSend + grp * (size_t)(32 * 512);
+        if (hl < heads) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<float4*>(src + (i * 128 + l) * 16) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(src + i * lanes16 + lane16) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+        if (grp == 0 && half == 0) reinterpret_cast<float2*>(smraw + kSendMl)[hl] = make_float2(M, L);
         fence_proxy_async_smem();
-        named_bar_sync(2 + cw, 128);
-        if (l == 0)
-          bulk_copy_to_peer(smraw + in_slot * (size_t)Mg::kPart + off, src, 32 * 512, &S.merged, (uint32_t)(2 * to) + rank);
+        named_bar_sync(2 + grp, 128);
+        if (l == 0 && heads > 0)
+          bulk_copy_to_peer(smraw + in_slot * (size_t)Mg::kPart + (col / 4) * lanes16, src, 8 * lanes16, &S.merged,
+                            (uint32_t)(2 * to) + rank);
+        if (grp == 0 && l < kSplits && l != sp)
+          bulk_copy_to_peer(smraw + kRecvMl + sp * (size_t)Mg::kMl, smraw + kSendMl, Mg::kMl, &S.merged,
+                            (uint32_t)(2 * l) + rank);
       }
-      float2* ml = reinterpret_cast<float2*>(smraw + kSendMl);
-      if (cw == 0 && half == 0) ml[hl] = make_float2(M, L);
-      fence_proxy_async_smem();
-      named_bar_sync(1, kSmThreads);
-      if (threadIdx.x < kSplits && threadIdx.x != sp)
-        bulk_copy_to_peer(smraw + kRecvMl + sp * (size_t)Mg::kMl, ml, Mg::kMl, &S.merged, 2 * threadIdx.x + rank);
-      bulk_commit();
-      const bool got = wait_local(&S.merged, 0, a.status, 57);
-      // out = sum_s w_s O_s / sum_s w_s l_s,  w_s = 2^(m_s - max m), splits in order
-      float w[kSplits];
-      float2 v[kSplits];
-      const float2 mine = make_float2(M, L);
-      M = -INFINITY;
-      L = 0.f;
+      if (grp < 4) {
+        constexpr int kMine = kCols / 4;            // columns of this thread: 32 or 16
+        const int col = kMine * grp;                // within the pair's columns
+        float own[kMine];
+        load_o(o_lane + sp * kCols + col, none, own);
+        const bool got = wait_local(&S.merged, 0, a.status, 57);
+        // out = sum_s w_s O_s / sum_s w_s l_s,  w_s = 2^(m_s - max m), splits in order
+        float w[kSplits];
+        float2 v[kSplits];
+        const float2 mine = make_float2(M, L);
+        M = -INFINITY;
+        L = 0.f;
 #pragma unroll
-      for (int s2 = 0; s2 < kSplits; ++s2) {
-        v[s2] = s2 == sp ? mine : reinterpret_cast<const float2*>(smraw + kRecvMl + s2 * (size_t)Mg::kMl)[hl];
-        M = fmaxf(M, v[s2].x);
-      }
-#pragma unroll
-      for (int s2 = 0; s2 < kSplits; ++s2) {
-        w[s2] = v[s2].x == -INFINITY ? 0.f : exp2f(v[s2].x - M);
-        L += w[s2] * v[s2].y;                     // NaN of a failed pair stays
-      }
-      const bool bad = named_bar_or(1, kSmThreads, !got) || L != L;
-      const float inv = L > 0.f ? 1.f / L : 0.f;
-      const int head = kHc * (int)rank + hl;
-      constexpr int kMine = kCols / 2;            // columns of this thread: 64 or 32
-#pragma unroll 1
-      for (int cc = 0; cc < kMine / 32; ++cc) {
-        const int col = kMine * cw + 32 * cc;     // within the pair's columns
-        float acc[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-#pragma unroll 1
         for (int s2 = 0; s2 < kSplits; ++s2) {
-          const float ws = s2 == 0 ? w[0] : s2 == 1 ? w[1] : s2 == 2 ? w[2 % kSplits] : w[3 % kSplits];
-          float o[32];
-          if (s2 == sp) {
-            load_o32(o_lane + sp * kCols + col, empty, o);
-          } else {
-            const uint8_t* src = smraw + (s2 < sp ? s2 : s2 - 1) * (size_t)Mg::kPart + (size_t)col * 512 + l * 16;
+          v[s2] = s2 == sp ? mine : reinterpret_cast<const float2*>(smraw + kRecvMl + s2 * (size_t)Mg::kMl)[hl];
+          M = fmaxf(M, v[s2].x);
+        }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 x = *reinterpret_cast<const float4*>(src + i * 2048);
+        for (int s2 = 0; s2 < kSplits; ++s2) {
+          w[s2] = v[s2].x == -INFINITY ? 0.f : exp2f(v[s2].x - M);
+          if (v[s2].y != v[s2].y) L = v[s2].y;      // a failed pair
+          L += w[s2] * v[s2].y;
+        }
+        const bool bad = named_bar_or(1, 4 * 128, !got || L != L);
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const int head = kHc * (int)rank + hl;
+        float acc[kMine];
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) acc[i] = 0.f;
+#pragma unroll
+        for (int s2 = 0; s2 < kSplits; ++s2) {
+          float o[kMine];
+          if (s2 == sp) {
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) o[i] = own[i];
+          } else {
+            const uint8_t* src = smraw + (s2 < sp ? s2 : s2 - 1) * (size_t)Mg::kPart + (col / 4) * lanes16 + (hl < heads ? lane16 : 0u);
+#pragma unroll
+            for (int i = 0; i < kMine / 4; ++i) {
+              const float4 x = *reinterpret_cast<const float4*>(src + i * lanes16);
               o[4 * i] = x.x, o[4 * i + 1] = x.y, o[4 * i + 2] = x.z, o[4 * i + 3] = x.w;
             }
           }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[i] = fmaf(ws, o[i], acc[i]);
+          for (int i = 0; i < kMine; ++i) acc[i] = fmaf(w[s2], o[i], acc[i]);
         }
         if (bad) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+          for (int i = 0; i < kMine; ++i) acc[i] = 0.f;
         }
         stage_bf16(smraw + Mg::kOut + (Mg::kTiles / 2 * half + (col >> 6)) * 8192, hl, sp * kCols + col, acc, inv);
-      }
-      if (a.lse && sp == 0 && cw == 0 && half == 0 && head < a.n_heads)
-        a.lse[(int64_t)t_out * a.n_heads + head] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
-      fence_proxy_async_smem();
-      named_bar_sync(1, kSmThreads);
-      if (threadIdx.x < Mg::kTiles && kHc * (int)rank < a.n_heads) {
-        const int i = threadIdx.x, in_half = i % (Mg::kTiles / 2), x = 256 * (i / (Mg::kTiles / 2)) + sp * kCols + 64 * in_half;
-        store_tile(&out_map, smraw + Mg::kOut + i * 8192, x, kHc * (int)rank, t_out);
-        bulk_commit();
+        fence_proxy_async_smem();
+        named_bar_sync(1, 4 * 128);
+        if (threadIdx.x < Mg::kTiles && kHc * (int)rank < a.n_heads) {
+          const int i = threadIdx.x, in_half = i % (Mg::kTiles / 2), x = 256 * (i / (Mg::kTiles / 2)) + sp * kCols + 64 * in_half;
+          store_tile(&out_map, smraw + Mg::kOut + i * 8192, x, kHc * (int)rank, t);
+          bulk_commit();
+        }
+        if (a.lse && sp == 0 && grp == 0 && half == 0 && head < a.n_heads)
+          a.lse[(int64_t)t * a.n_heads + head] = L > 0.f && !bad ? (M + log2f(L)) * kLn2 : -INFINITY;
       }
     }
+    // what the CTAs sent one another has been received, or was released at the barrier before
+    bulk_wait_read0();
+    tc_fence_before();
+    __syncwarp();
+    cluster_arrive_relaxed();
   }
-  // this thread's copies are done before shared memory goes
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();                       // no access to the pair's memory is still pending
+  // nothing of the cluster is still to be accessed behind this barrier
+  cluster_wait();
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);

@@ -595,6 +595,11 @@ __device__ __forceinline__ void load_o(uint32_t taddr, bool empty, float (&o)[N]
   tmem_wait_ld();
 }
 
+// Of a row's sum of weights: 0 for no key at all, NaN for a NaN logit or a wait that ran
+// out, and 1 or so otherwise (its largest term is 2^-8 at least).
+__device__ __forceinline__ float inverse_sum(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
+__device__ __forceinline__ float log_sum(float m, float sum) { return sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2; }
+
 // Two fp32 in one 64-bit register pair: one instruction for both.
 __device__ __forceinline__ uint64_t pair_f32(float a, float b) {
   uint64_t r;
@@ -820,16 +825,13 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_c
       settled = settled && !bad;
       tc_fence_after();
       const float M = empty ? -INFINITY : S.m_run[last][hl];
-      S.red[g][l] = sm.m == -INFINITY ? 0.f : sm.sum * exp2f(sm.m - M);
-      if (kSplits > 1) {
-        // NaN marks the row for whoever takes part in the merge, in the other pairs too
-        if (bad) S.red[g][l] = __int_as_float(0x7FC00000);
-        break;
-      }
+      // (a maximum of -inf goes with a sum of 0, or NaN from a NaN logit, which stays)
+      S.red[g][l] = bad ? __int_as_float(0x7FC00000) : sm.m == -INFINITY ? sm.sum : sm.sum * exp2f(sm.m - M);
+      if (kSplits > 1) break;
       named_bar_sync(1, kSmThreads);
       const float L = (S.red[0][hl] + S.red[1][hl]) + (S.red[0][hl + 64] + S.red[1][hl + 64]);
       named_bar_sync(1, kSmThreads);              // read before the next row's maxima go there
-      const float inv = L > 0.f ? 1.f / L : 0.f;
+      const float inv = inverse_sum(L);
       if (empty) {
         // the values' tiles may hold a later row's already: zeros go out directly
         uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)t_out * a.n_heads * kDC);
@@ -866,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_c
         __syncwarp();
       }
       if (a.lse && half == 0 && g == 0 && head < a.n_heads)
-        a.lse[(int64_t)t_out * a.n_heads + head] = L > 0.f && !bad ? (M + log2f(L)) * kLn2 : -INFINITY;
+        a.lse[(int64_t)t_out * a.n_heads + head] = log_sum(M, L);
     }
     if (kSplits == 1) {
       // A release would wait for the output's stores as well (1,500 cycles).  There is no
@@ -900,14 +902,13 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_c
       const bool none = r.nblk == 0;
       float M = none ? -INFINITY : S.m_run[(r.nblk - 1) & 1][hl];
       float L = (S.red[0][hl] + S.red[1][hl]) + (S.red[0][hl + 64] + S.red[1][hl + 64]);
-      const bool fail = __any_sync(0xffffffffu, L != L);
       // a column group's 16 bytes of every lane that travels; this lane's place there
       const uint32_t lanes16 = 32u * heads, lane16 = 16u * (half * heads + hl);
       if (grp < kItems) {
         const int dst = grp * 32 / kCols, to = dst < sp ? dst : dst + 1, in_slot = sp < to ? sp : sp - 1;
         const int col = grp * 32 % kCols;
         float o[32];
-        load_o(o_lane + to * kCols + col, none || fail, o);
+        load_o(o_lane + to * kCols + col, none, o);
         uint8_t* src = smraw + kSend + grp * (size_t)(32 * 512);
         if (hl < heads) {
 #pragma unroll
@@ -944,11 +945,10 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_c
 #pragma unroll
         for (int s2 = 0; s2 < kSplits; ++s2) {
           w[s2] = v[s2].x == -INFINITY ? 0.f : exp2f(v[s2].x - M);
-          if (v[s2].y != v[s2].y) L = v[s2].y;      // a failed pair
-          L += w[s2] * v[s2].y;
+          L += w[s2] * v[s2].y;                     // NaN stays
         }
-        const bool bad = named_bar_or(1, 4 * 128, !got || L != L);
-        const float inv = L > 0.f ? 1.f / L : 0.f;
+        if (named_bar_or(1, 4 * 128, !got)) L = __int_as_float(0x7FC00000);
+        const float inv = inverse_sum(L);
         const int head = kHc * (int)rank + hl;
         float acc[kMine];
 #pragma unroll
@@ -970,10 +970,6 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_c
 #pragma unroll
           for (int i = 0; i < kMine; ++i) acc[i] = fmaf(w[s2], o[i], acc[i]);
         }
-        if (bad) {
-#pragma unroll
-          for (int i = 0; i < kMine; ++i) acc[i] = 0.f;
-        }
         stage_bf16(smraw + Mg::kOut + (Mg::kTiles / 2 * half + (col >> 6)) * 8192, hl, sp * kCols + col, acc, inv);
         fence_proxy_async_smem();
         named_bar_sync(1, 4 * 128);
@@ -983,7 +979,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_c
           bulk_commit();
         }
         if (a.lse && sp == 0 && grp == 0 && half == 0 && head < a.n_heads)
-          a.lse[(int64_t)t * a.n_heads + head] = L > 0.f && !bad ? (M + log2f(L)) * kLn2 : -INFINITY;
+          a.lse[(int64_t)t * a.n_heads + head] = log_sum(M, L);
       }
     }
     // what the CTAs sent one another has been received, or was released at the barrier before

@@ -229,3 +229,37 @@ def test_capture_replay_and_second_stream(N):
         lens, table, free = want["seq_len"], want["block_table"], want["free_list"]
     p.check(want)
     assert p.status() == (0, -1)
+
+
+def test_workspace_shared_with_other_calls(N):
+    """Plans between appends, reads and attention on one workspace, all on one stream."""
+    import torch
+    rng = np.random.default_rng(8)
+    lens, table, free, pages = make_state(rng, 6, 64, 20, 30)
+    pl = Plan(N, lens, table, free, pages, 64, 3000, in_place=True)
+    nb = 1 << 20
+    ws = torch.zeros(nb, dtype=torch.uint8, device="cuda")
+    pl.ws, pl.nb = ws, nb
+    d = N.dsa_dims(n_idx_heads=64, d_idx=128, n_heads=128, d_c=512, d_r=64, topk=64, idx_dtype=N.DSA_FP8_E4M3,
+                   mla_dtype=N.DSA_INT4, sm_scale=0.05, algo=0)
+    lat = torch.zeros((pages * 64, N.dsa_latent_row_bytes(d)), dtype=torch.uint8, device="cuda")
+    ik, isc = torch.zeros((pages * 64, 128), dtype=torch.uint8, device="cuda"), torch.zeros(pages * 64, device="cuda")
+    cache = N.dsa_cache(latent=lat.data_ptr(), idx_k=ik.data_ptr(), idx_k_scale=isc.data_ptr(), block_table=pl.table.data_ptr(),
+                        page_size=64, max_pages_per_seq=table.shape[1], num_seqs=6, num_tokens=pages * 64)
+    k = torch.ones((3000, 128), device="cuda")
+    new = torch.ones((3000, 576), dtype=torch.bfloat16, device="cuda")
+    back = torch.empty_like(new)
+    cur = dict(seq_len=lens, block_table=table, free_list=free)
+    for step in range(4):
+        n_new = rng.integers(0, 40, 6)
+        want = R.batch_plan(cur["seq_len"], n_new, None, cur["free_list"], cur["block_table"], 64, pages, 3000)
+        pl.run(n_new)
+        slot = pl.out["slot"].data_ptr()
+        N.dsa_cache_append_slots(d, cache, 3000, slot, k.data_ptr(), new.data_ptr(), ws.data_ptr(), nb, pl.stream)
+        back.fill_(7)
+        N.dsa_cache_read(d, cache, 3000, slot, None, back.data_ptr(), ws.data_ptr(), nb, pl.stream)
+        n = int(pl.totals[0])
+        assert n == len(want["rows"]) > 0
+        assert (back[:n, 512:] == 1).all() and (back[n:] == 7).all()
+        assert pl.status() == (0, -1)
+        cur = want

@@ -356,3 +356,77 @@ def test_many_rows_of_every_length(N, seed):
     first = [x.copy() for x in c.result()]
     for x, y in zip(first, c.call().result()):
         np.testing.assert_array_equal(x, y)
+
+
+@pytest.mark.parametrize("H", [1, 5, 63, 65, 127])
+@pytest.mark.parametrize("T", [2, 21, 80])
+def test_any_number_of_heads(N, H, T):
+    """Rows merged from four, two and no key splits, heads that are no multiple of 8."""
+    c = Case(N, [200 + 7 * t for t in range(T)], H=H, topk=300, seed=H + T).build().call()
+    assert c.ran() & N.DSA_KERNEL_MLA_INT4_TC and c.status() == (0, -1)
+    c.check(rows=sorted({0, 1, T // 2, T - 1}))
+
+
+@pytest.mark.parametrize("T", [2, 21, 80])
+def test_nan_and_infinite_queries_stay_with_their_head(N, T):
+    c = Case(N, [500 + t for t in range(T)], topk=256, seed=T)
+    c.q[0, 3, 5], c.q[1, 70, 575], c.q[T - 1, 127, 0] = 0x7FC0, 0x7F80, 0xFF80
+    bad = [(0, 3), (1, 70), (T - 1, 127)]
+    c.build().call()
+    out, lse = c.result()
+    assert c.status() == (0, -1)
+    for t, h in bad:
+        assert np.isnan(out[t, h]).all() and np.isnan(lse[t, h]), (t, h)
+    keep = np.ones((T, 128), bool)
+    keep[tuple(np.array(bad).T)] = False
+    assert np.isfinite(out[:T][keep]).all() and np.isfinite(lse[:T][keep]).all()
+    clean = Case(N, [500 + t for t in range(T)], topk=256, seed=T).build().call()
+    o2, l2 = clean.result()
+    np.testing.assert_array_equal(out[:T][keep], o2[:T][keep])
+    np.testing.assert_array_equal(lse[:T][keep], l2[:T][keep])
+    clean.check(rows=[0, T - 1])
+
+
+def test_two_streams_at_once(N):
+    """Two calls in flight on two streams, each with a workspace of its own."""
+    import torch
+    a = Case(N, [1500 + 3 * t for t in range(40)], topk=1024, seed=1).build()
+    b = Case(N, [900 + 5 * t for t in range(9)], H=40, topk=512, seed=2).build()
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(20):
+        with torch.cuda.stream(s1):
+            a.call()
+        with torch.cuda.stream(s2):
+            b.call()
+    torch.cuda.synchronize()
+    a.check(rows=[0, 39]), b.check(rows=[0, 8])
+    assert a.status() == b.status() == (0, -1)
+
+
+FIRST = """
+import sys
+sys.path.insert(0, {root!r})
+import torch
+from tests.test_int4_mla_gpu import Case
+from long_context_sparse_04_b200 import _native as N
+c = Case(N, [700] * {T}, topk=512).build()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    c.call()
+for _ in range(2):
+    g.replay()
+c.check(rows=[0, {T} - 1])
+assert c.status() == (0, -1)
+"""
+
+
+@pytest.mark.parametrize("T", [1, 80])
+def test_first_call_of_a_process_is_captured(N, T):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", FIRST.format(root=root, T=T)], cwd=root, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stderr[-2000:]

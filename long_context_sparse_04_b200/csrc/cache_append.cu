@@ -77,7 +77,7 @@ __device__ __forceinline__ uint32_t amax_bf16(const uint4& x, const uint4& y) {
   const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
   uint32_t m = w[0] & 0x7FFF7FFFu;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+  for (int i = 1; i < 8; ++i) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7FFF7FFFu));
   return max(m & 0xFFFFu, m >> 16);
 }
 
@@ -127,6 +127,44 @@ __device__ __forceinline__ bool position_row(const AppendArgs& a, int seq, int p
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// Two fp32 in one 64-bit register pair: one instruction for both.
+__device__ __forceinline__ uint64_t pair_f32(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// The code words of a group whose scale's reciprocal is r.
+__device__ __forceinline__ void int4_codes(const uint32_t (&v)[8], float r, uint32_t (&w)[2]) {
+  const uint64_t r2 = pair_f32(r, r), to_grid = pair_f32(6144.f, 6144.f), to_int = pair_f32(12576768.f, 12576768.f);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t x = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t p = v[4 * h + i];
+      uint64_t c = mul_f32x2(pair_f32(bf16_lo(p), bf16_hi(p)), r2);
+      // (c + 6144) - 6144 + 1.5 * 2^23: the low bits are the code in two's complement,
+      // rounded to even (the last two constants are one, exactly)
+      c = add_f32x2(add_f32x2(c, to_grid), to_int);
+      // nibble i of each half
+      const uint32_t q = __byte_perm((uint32_t)c, (uint32_t)(c >> 32), 0x5410), keep = 0x00010001u * ((1u << (4 * i)) - 1u);
+      x = (x & keep) | ((q << (4 * i)) & ~keep);
+    }
+    w[h] = x;
+  }
+}
+
 // One group of 16 latent dims (eight bf16 pairs) as its scale byte and two code
 // words: the scale is fl32(amax / 7) rounded to 8 bits, the code the nearest integer
 // to c / scale, ties to even, within +-7.
@@ -141,31 +179,23 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // c * rcp(scale) is within 2e-6 of it below 8, so rounding that product to a multiple of
 // 2^-11 (adding 6144) restores ties exactly and moves nothing else across one.
 // `amax`: the largest |c| as a bf16 pattern.
-__device__ __forceinline__ uint32_t int4_group(const uint32_t (&v)[8], uint32_t amax, uint32_t (&w)[2]) {
+__device__ __forceinline__ uint32_t int4_group(uint32_t (&v)[8], uint32_t amax, uint32_t (&w)[2]) {
   const float a7 = bf16_lo(amax) * (1.f / 7.f);
   const uint32_t code = scale_code(__uint_as_float((__float_as_uint(a7) + 8u) & ~15u));
   w[0] = w[1] = 0u;
   if (code == 0u) return 0u;
-  const float r = rcp_approx(scale_value(code));
-  // a normal, unsaturated scale is at least 16/17 of amax / 7: quotients stay below 7.5
-  const bool clamp = code < 8u || code == kScaleMax;
-  uint32_t q[8];
+  const float scale = scale_value(code), r = rcp_approx(scale);
+  // a normal, unsaturated scale is at least 16/17 of amax / 7, so quotients stay below
+  // 7.5; with other scales the dims are clamped to 7 of them first (exact: a bf16)
+  if (code < 8u || code == kScaleMax) {
+    const uint32_t top = __float_as_uint(7.f * scale) >> 16, hi = __byte_perm(top, top, 0x1010), lo = hi | 0x80008000u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float c0 = bf16_lo(v[i]) * r, c1 = bf16_hi(v[i]) * r;
-    if (clamp) {
-      c0 = fminf(fmaxf(c0, -7.f), 7.f);
-      c1 = fminf(fmaxf(c1, -7.f), 7.f);
+    for (int i = 0; i < 8; ++i) {
+      asm("min.bf16x2 %0, %0, %1;" : "+r"(v[i]) : "r"(hi));
+      asm("max.bf16x2 %0, %0, %1;" : "+r"(v[i]) : "r"(lo));
     }
-    // (c + 6144) - 6144 + 1.5 * 2^23: the low bits are the code in two's complement,
-    // rounded to even (the last two constants are one, exactly)
-    const uint32_t q0 = __float_as_uint(__fadd_rn(__fadd_rn(c0, 6144.f), 12576768.f));
-    const uint32_t q1 = __float_as_uint(__fadd_rn(__fadd_rn(c1, 6144.f), 12576768.f));
-    q[i] = __byte_perm(q0, q1, 0x5410) & 0x000F000Fu;
   }
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    w[h] = q[4 * h] | (q[4 * h + 1] << 4) | (q[4 * h + 2] << 8) | (q[4 * h + 3] << 12);
+  int4_codes(v, r, w);
   return code;
 }
 
@@ -262,10 +292,11 @@ cache_append_kernel(const AppendArgs a) {
 }
 
 // Packed rows.  A lane quantises whole groups of 16 latent dims (d_c = 512: one each),
-// so a group's maximum needs no exchange.  65,536 tokens take 42 us against a floor of
+// so a group's maximum needs no exchange.  65,536 tokens take 39 us against a floor of
 // 22 us for their 146 MB: what bounds it is the integer pipe (unpacking, packing and
-// comparing; a warp instruction takes it two cycles).  Persistent warps with the next
-// token's loads in flight, and more CTAs a SM at fewer registers, measured the same.
+// comparing; a warp instruction takes it two cycles): fp32 pairs and bf16 pair maxima
+// took it from 42.4 to 39.2.  Persistent warps with the next token's loads in flight
+// measured the same, four CTAs an SM without the spills 41.3.
 struct Token {
   float4 key;              // this lane's first key chunk (d_I > 128: the others are loaded late)
   uint4 lat[2], rope;      // its group of 16 dims, its piece of the RoPE key
@@ -326,6 +357,10 @@ __device__ __forceinline__ void store_token(const AppendArgs& a, int64_t n, cons
     if (lane == 0) set_status(a.status, DSA_ERR_INVALID_ARG, (int)n);
     return;
   }
+  const Int4Row ly = int4_row(a.d_c, a.d_r);
+  const int groups = a.d_c / kInt4Group, pieces = a.d_r >> 3;
+  uint8_t* dst = static_cast<uint8_t*>(a.latent) + row * a.latent_row_bytes;
+  if (a.latent_new != nullptr && lane < pieces) reinterpret_cast<uint4*>(dst + ly.rope)[lane] = x.rope;
   if (kc > 0) {
     if (a.idx_dtype == DSA_FP8_E4M3) {
       const float s = key_scale(amax);
@@ -340,17 +375,13 @@ __device__ __forceinline__ void store_token(const AppendArgs& a, int64_t n, cons
     }
   }
   if (a.latent_new == nullptr) return;
-  const Int4Row ly = int4_row(a.d_c, a.d_r);
-  const int groups = a.d_c / kInt4Group, pieces = a.d_r >> 3;
-  uint8_t* dst = static_cast<uint8_t*>(a.latent) + row * a.latent_row_bytes;
   if (lane < groups) {
-    const uint32_t v[8] = {x.lat[0].x, x.lat[0].y, x.lat[0].z, x.lat[0].w, x.lat[1].x, x.lat[1].y, x.lat[1].z, x.lat[1].w};
+    uint32_t v[8] = {x.lat[0].x, x.lat[0].y, x.lat[0].z, x.lat[0].w, x.lat[1].x, x.lat[1].y, x.lat[1].z, x.lat[1].w};
     uint32_t w[2];
     const uint32_t code = int4_group(v, lat_max, w);
     reinterpret_cast<uint2*>(dst)[lane] = make_uint2(w[0], w[1]);
     dst[ly.scale + lane] = (uint8_t)code;
   }
-  if (lane < pieces) reinterpret_cast<uint4*>(dst + ly.rope)[lane] = x.rope;
   const uint4* rsrc = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.latent_new) + n * a.latent_new_row_bytes) + 2 * groups;
   for (int c = lane + 32; c < pieces; c += 32) reinterpret_cast<uint4*>(dst + ly.rope)[c] = ld_stream_u4(rsrc + c);
   const int pad = ly.scale + groups + lane;

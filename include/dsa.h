@@ -92,8 +92,9 @@ typedef enum {
  * turn on its exact phases, and it is 128 of the 416 bytes. */
 
 /* Which kernels to run.  AUTO picks the tensor-core kernels (tcgen05) for the
- * FP8 indexer with H_I*group <= 256, d_I = 128, and for bf16 MLA with
- * H = 128, d_c = 512, d_r = 64; everything else runs the SIMT kernels.  With
+ * FP8 indexer with H_I*group <= 256, d_I = 128, for bf16 MLA with H = 128,
+ * d_c = 512, d_r = 64, and for MLA over int4 latents with any H <= 128,
+ * d_c = 512, d_r = 64; everything else runs the SIMT kernels (H a multiple of 8).  With
  * AUTO, dsa_decode_step and dsa_forward fuse the indexer and top-k when the
  * tensor-core indexer runs and q_group <= 2: the indexer's epilogue also
  * builds each row's histogram of its scores' top 12 order-preserving key bits
@@ -239,7 +240,9 @@ dsa_status dsa_set_stage_events(void* const* events, int32_t n_events);
  * kernels record clock64() stamps of their pipeline events there, each in its
  * own region: int64 [0, 512) the sparse-MLA kernel's first CTA pair
  * ([2 CTAs][8 events][32 blocks]: decoded, after the max barrier, S issued,
- * PV issued, S read by the softmax, peer logits arrived, P stored, exp done),
+ * PV issued, S read by the softmax, peer logits arrived, P stored, exp done;
+ * over int4 latents: keys decoded, values decoded, S issued, PV issued, S
+ * arrived at the softmax, keys' stage free, P stored, values' stage free),
  * [512, 640) top-k's first cluster ([8 CTAs][16 events], phase ends; the
  * cluster kernel only), and
  * [640, 896) the indexer's CTA 0 ([8 events][32 tiles]: stage free, TMA
@@ -290,7 +293,9 @@ dsa_status dsa_topk(const dsa_dims* dims, const dsa_rows* rows, const float* sco
 /* Stage 3: sparse absorbed MLA over the selected rows.
  *   q   [T, H, d_c + d_r] bf16 (DSA_BF16, DSA_INT4) | f32
  *   idx [T, topk] int32 logical positions (entries < 0 are skipped; entries
- *       >= klen[t] are a caller error and are read as given)
+ *       >= klen[t] are a caller error: read as given by the SIMT kernels,
+ *       skipped by the tensor-core kernels, which also read no more than the
+ *       first klen[t] entries, as dsa_topk leaves them)
  *   out [T, H, d_c] bf16 | f32 (same dtype as q)
  *   lse [T, H] fp32 natural-log sum of exp(z) (may be NULL); -inf and out = 0
  *       for a row with no selected key. */
@@ -303,7 +308,7 @@ dsa_status dsa_sparse_mla_fwd(const dsa_dims* dims, const dsa_rows* rows, const 
  * call: it is a deployment convenience.  Arguments, layouts and results are
  * those of dsa_sparse_mla_fwd, bit for bit (same kernels, same split plan).
  * Scratch: a file-scope static device array of 20 MiB (256-byte status block
- * + split-K partials) inside the library.  Nothing is allocated: no
+ * + split-K partials; int4 latents need no partials) inside the library.  Nothing is allocated: no
  * cudaMalloc/cudaFree, no allocating library routine.
  *   - The first call on each device looks up the array's device address
  *     (cudaGetSymbolAddress, with that device current) and keeps it; make that
@@ -467,7 +472,10 @@ typedef struct {
  * request longer than its row of the block table (refused), and for a page id
  * outside the cache, whose block-table entry and slots become -1.
  * B <= 16384 and B * max_pages_per_seq < 2^31.  Deterministic; one kernel.
- * ws: dsa_workspace_size(NULL, NULL, DSA_OP_BATCH_PLAN) bytes (the status block). */
+ * ws: dsa_workspace_size(NULL, NULL, DSA_OP_BATCH_PLAN) bytes (the status block),
+ * zeroed once by dsa_workspace_init: its CTAs count themselves there, so the plan
+ * of a workspace never zeroed may leave seq_len_out, free_count_out and totals
+ * unwritten, and plans that may overlap need workspaces of their own. */
 dsa_status dsa_batch_plan(const dsa_cache* cache, const dsa_plan* plan, void* ws, size_t ws_bytes,
                           dsa_stream_t stream);
 

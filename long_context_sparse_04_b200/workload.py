@@ -240,11 +240,17 @@ class DevicePlanner:
     def stream(self):
         return ctypes.c_void_p(self.torch.cuda.current_stream(self.device).cuda_stream)
 
+    def on_device(self):
+        """The library launches on the current device: this makes it the planner's."""
+        return self.torch.cuda.device(self.device)
+
     def plan(self):
-        N.dsa_batch_plan(self.cache, self._plan, _vp(self._ws), self._ws.numel(), self.stream)
+        with self.on_device():
+            N.dsa_batch_plan(self.cache, self._plan, _vp(self._ws), self._ws.numel(), self.stream)
 
     def status(self):
-        return N.dsa_read_device_status(_vp(self._ws), self.stream)
+        with self.on_device():
+            return N.dsa_read_device_status(_vp(self._ws), self.stream)
 
     def rows(self, q_group: int = 1):
         """dsa_rows of the whole (padded) batch."""
@@ -275,26 +281,30 @@ class PagedCache:
                                  max_pages_per_seq=p.cache.max_pages_per_seq, num_seqs=p.num_seqs, num_tokens=n)
         self.rows = p.rows(q_group)
         self.idx = torch.full((p.max_tokens, topk), -1, dtype=torch.int32, device=dev)
-        nb = N.dsa_workspace_size(self.dims, self.rows, N.DSA_OP_DECODE_STEP)
-        self._ws = torch.empty(nb, dtype=torch.uint8, device=dev)
-        N.dsa_workspace_init(_vp(self._ws), nb, p.stream)
+        with p.on_device():
+            nb = N.dsa_workspace_size(self.dims, self.rows, N.DSA_OP_DECODE_STEP)
+            self._ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+            N.dsa_workspace_init(_vp(self._ws), nb, p.stream)
 
     def _args(self):
         return _vp(self._ws), self._ws.numel(), self.planner.stream
 
     def append(self, k_new, latent_new):
         """The planned step's tokens (rows of max_tokens) into the caches."""
-        N.dsa_cache_append_slots(self.dims, self.cache, self.planner.max_tokens, _vp(self.planner.slot), _vp(k_new),
-                                 _vp(latent_new), *self._args())
+        with self.planner.on_device():
+            N.dsa_cache_append_slots(self.dims, self.cache, self.planner.max_tokens, _vp(self.planner.slot), _vp(k_new),
+                                     _vp(latent_new), *self._args())
 
     def read(self, slot, k_out=None, latent_out=None):
         """Cached tokens by physical row, as the values they stand for."""
-        N.dsa_cache_read(self.dims, self.cache, int(slot.shape[0]), _vp(slot), _vp(k_out), _vp(latent_out), *self._args())
+        with self.planner.on_device():
+            N.dsa_cache_read(self.dims, self.cache, int(slot.shape[0]), _vp(slot), _vp(k_out), _vp(latent_out), *self._args())
 
     def decode_step(self, q_idx, q_scale, w, q, out, lse=None):
         """The three stages over the planned rows; rows behind the last give 0 and -inf."""
-        N.dsa_decode_step(self.dims, self.rows, self.cache, _vp(q_idx), _vp(q_scale), _vp(w), _vp(q), _vp(out), _vp(lse),
-                          None, _vp(self.idx), *self._args())
+        with self.planner.on_device():
+            N.dsa_decode_step(self.dims, self.rows, self.cache, _vp(q_idx), _vp(q_scale), _vp(w), _vp(q), _vp(out), _vp(lse),
+                              None, _vp(self.idx), *self._args())
         return out, lse
 
     def indices(self):
@@ -302,4 +312,5 @@ class PagedCache:
         return self.idx
 
     def status(self):
-        return N.dsa_read_device_status(*self._args()[::2])
+        with self.planner.on_device():
+            return N.dsa_read_device_status(*self._args()[::2])

@@ -25,7 +25,7 @@
 // both for itself straight from the packed rows: at three instructions a pair of
 // values that is cheaper than an exchange through distributed shared memory.
 //
-// Roles per CTA (832 threads):
+// Roles per CTA (864 threads):
 //   warps 0-7    softmax and output, two groups of four warps that take the blocks in
 //                turn: a block's chain (wait, tensor-memory load, maximum, weights,
 //                store) is longer than its products take, so one group would set the
@@ -39,7 +39,7 @@
 //                set the pace), then 16-byte stores, swizzled, of the keys' and the
 //                values' tile
 //   warp 24      tensor memory; in the pair's first CTA one thread issues the MMAs
-//   warp 25      resolves the selection to cache rows, up to four blocks ahead
+//   warps 25-26  resolve the selection to cache rows, up to four blocks ahead
 // Tiles, weights and logits have two stages each; S of block j+1 is issued before
 // P V of block j, so that the tensor cores work while the softmax of block j runs.
 // Without key splits the kernel is persistent: a pair takes rows t, t + pairs, ...,
@@ -64,8 +64,8 @@ constexpr int kBlk = 64, kHalfBlk = 32;
 constexpr int kMaxKeys = 2048;
 constexpr int kMaxPairs = 4;                    // key splits of a row: 1, 2 or 4 (a cluster of 8 CTAs)
 constexpr int kSmWarps = 8, kDecWarps = 8;
-constexpr int kDecWarp0 = 8, kMmaWarp = 24, kRowWarp = 25;
-constexpr int kThreads = 32 * 26;
+constexpr int kDecWarp0 = 8, kMmaWarp = 24, kRowWarp = 25, kRowWarps = 2;
+constexpr int kThreads = 32 * (kRowWarp + kRowWarps);
 constexpr int kSmThreads = 32 * kSmWarps;
 constexpr int kDecThreads = 2 * kDecWarps * 32;
 constexpr int kQChunks = kD / 64;               // 64-dim SW128 chunks: 8 latent, 1 RoPE
@@ -89,7 +89,7 @@ struct Smem {                                   // 1024-byte aligned
   // waited for by the issuing thread, in the pair's first CTA
   uint64_t q_full, k_full[2], v_full[2], p_full[2], o_free;
   // arrivals of finished products, in both CTAs
-  uint64_t s_full[2], pv_done[2];
+  uint64_t s_full[2], pv_done[2], q_idle;       // q_idle: every S of a row
   uint64_t rows_full[kRowRing], rows_free[kRowRing];
   uint64_t merged;                              // the other splits' parts have arrived
   uint64_t v_idle[2];                           // the row's output has left a stage of the values' tiles
@@ -287,6 +287,7 @@ __device__ __forceinline__ void issue_products(Smem& S, RowStream<kSplits> rows,
             mma_bf16_pair(d, qd + (ch * kHc * 128 + 32 * kk >> 4), kd + (ch * kHalfBlk * 128 + 32 * kk >> 4), idesc_s,
                           (ch | kk) != 0);
         mma_commit_pair(&S.s_full[b], mask);
+        if (kSplits == 1 && j + 1 == r.nblk) mma_commit_pair(&S.q_idle, mask);
         tstamp(a.trace, 0, 2, n);
       }
       if (j >= 1) {
@@ -316,22 +317,20 @@ __device__ __forceinline__ void issue_products(Smem& S, RowStream<kSplits> rows,
 }
 
 // ---------------------------------------------------------------- the selection
-// One warp turns the selection into cache rows, two keys of a block per lane: the
-// block-table entries of one block and the positions of the next are in flight while
-// the block before is handed over.
+// Two warps turn the selection into cache rows, the blocks of parity p each, two keys of
+// a block per lane: the positions of a warp's next block are in flight with the
+// block-table entries of this one.  (One warp took 2,000 cycles a block, longer where
+// the selection came from HBM, and set the pace: a prefill of 2,048 rows 1.33 ms
+// instead of 1.14.  What is being loaded is neither copied nor tested before it is
+// used, for either would wait for it.)
 template <int kSplits>
-__device__ __forceinline__ void resolve_rows(Smem& S, RowStream<kSplits> rows, uint32_t rank) {
+__device__ __forceinline__ void resolve_rows(Smem& S, RowStream<kSplits> rows, uint32_t rank, int p) {
   const MlaArgs& a = rows.a;
   const CacheMap& m = a.map;
   const int lane = threadIdx.x & 31;
-  struct Keys {
-    int s[2], e[2];                               // positions, block-table entries
-    int seq;
-    bool any;                                     // a block at all
-  };
   // The first block's positions, where a full selection has them, go to L1 while the
   // row's length is on its way.
-  const int guess = (a.topk + kSplits * kBlk - 1) / (kSplits * kBlk) * kBlk * rows.sp + lane;
+  const int guess = (a.topk + kSplits * kBlk - 1) / (kSplits * kBlk) * kBlk * rows.sp + kBlk * p + lane;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     int32_t unused;
@@ -342,82 +341,76 @@ __device__ __forceinline__ void resolve_rows(Smem& S, RowStream<kSplits> rows, u
   r.nblk = 0;
   int j = 0;
   bool more = rows.next_busy(r);
-  const auto positions = [&](Keys& x) {
-    x.any = more;
-    x.s[0] = x.s[1] = -1;
-    x.seq = r.seq;
-    if (!more) return;
-    const int32_t* idx = a.idx + (int64_t)rows.t * a.topk + r.k0;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int i = j * kBlk + 32 * u + lane;
-      if (i < r.nvalid) x.s[u] = __ldg(idx + i);
-      if (x.s[u] >= r.klen) x.s[u] = -1;
-    }
-    if (++j == r.nblk) {
+  const auto advance = [&] {
+    if (more && ++j == r.nblk) {
       j = 0;
       more = rows.next_busy(r);
       // the next row's Q comes to L2 some blocks before its tile is free: every pair
       // changes rows at about the same time, and from HBM that took 11,000 cycles
       const int heads = min(kHc, a.n_heads - kHc * (int)rank);
-      if (more && heads > 0 && lane == 0)
+      if (more && heads > 0 && p == 0 && lane == 0)
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
                          static_cast<const __nv_bfloat16*>(a.q) + ((int64_t)rows.t * a.n_heads + kHc * (int)rank) * kD),
                      "r"(heads * kD * 2) : "memory");
     }
   };
-  const auto page_of = [&](int s) { return m.page_shift >= 0 ? s >> m.page_shift : s / m.page_size; };
-  const auto entries = [&](Keys& x) {
+  int s[2], seq = 0, klen = 0;                    // the next block's positions and row
+  bool any = false;
+  const auto positions = [&] {
+    any = more;
+    if (!more) return;
+    seq = r.seq;
+    klen = r.klen;
+    const int32_t* idx = a.idx + (int64_t)rows.t * a.topk + r.k0;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      x.e[u] = -1;
-      if (x.s[u] < 0) continue;
+      const int i = j * kBlk + 32 * u + lane;
+      s[u] = -1;
+      if (i < r.nvalid) s[u] = __ldg(idx + i);
+    }
+    advance();
+    advance();                                    // the other warp's block
+  };
+  if (p == 1) advance();
+  positions();
+  for (int n = p; any; n += 2) {
+    int e[2], off[2];
+    bool has[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      has[u] = s[u] >= 0 && s[u] < klen;
+      off[u] = s[u];
+      e[u] = 0;
       if (m.block_table != nullptr) {
-        const int pg = page_of(x.s[u]);
-        if (pg < m.max_pages_per_seq) x.e[u] = __ldg(m.block_table + (int64_t)x.seq * m.max_pages_per_seq + pg);
-        else set_status(a.status, DSA_ERR_OUT_OF_RANGE, x.s[u]);
-      } else {
-        x.e[u] = m.seq_start != nullptr ? __ldg(m.seq_start + x.seq) : 0;
+        const int pg = m.page_shift >= 0 ? s[u] >> m.page_shift : s[u] / m.page_size;
+        off[u] -= pg * m.page_size;
+        if (has[u] && pg >= m.max_pages_per_seq) {
+          set_status(a.status, DSA_ERR_OUT_OF_RANGE, s[u]);
+          has[u] = false;
+        }
+        if (has[u]) e[u] = __ldg(m.block_table + (int64_t)seq * m.max_pages_per_seq + pg);
+      } else if (has[u] && m.seq_start != nullptr) {
+        e[u] = __ldg(m.seq_start + seq);
       }
     }
-  };
-  const auto row = [&](int s, int e) {
-    if (s < 0) return -1;
-    if (m.block_table != nullptr) {
-      const int pg = page_of(s);
-      if (pg >= m.max_pages_per_seq) return -1;
-      if (e < 0 || e >= m.num_pages) {
-        set_status(a.status, DSA_ERR_OUT_OF_RANGE, e);
-        return -1;
-      }
-      return (int)((int64_t)e * m.page_size + (s - pg * m.page_size));
-    }
-    const int64_t x = (int64_t)e + s;
-    if (x < 0 || x >= m.num_tokens) {
-      set_status(a.status, DSA_ERR_OUT_OF_RANGE, s);
-      return -1;
-    }
-    return (int)x;
-  };
-  Keys x, y, z;
-  positions(x);
-  positions(y);
-  entries(x);
-  for (int n = 0; x.any; ++n) {
-    positions(z);
-    entries(y);
+    positions();
     const int slot = n % kRowRing;
     if (!wait_warp(&S.rows_free[slot], (n / kRowRing & 1) ^ 1, a.status, 53)) break;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int rw = row(x.s[u], x.e[u]);
-      S.rows[slot][32 * u + lane] = rw;
-      const uint32_t bits = __ballot_sync(0xffffffffu, rw >= 0);
+      int64_t row = (int64_t)e[u] + off[u];
+      bool in = row >= 0 && row < m.num_tokens;
+      if (m.block_table != nullptr) {
+        in = e[u] >= 0 && e[u] < m.num_pages;
+        row = (int64_t)e[u] * m.page_size + off[u];
+      }
+      if (has[u] && !in) set_status(a.status, DSA_ERR_OUT_OF_RANGE, m.block_table != nullptr ? e[u] : off[u]);
+      const bool ok = has[u] && in;
+      S.rows[slot][32 * u + lane] = ok ? (int)row : -1;
+      const uint32_t bits = __ballot_sync(0xffffffffu, ok);
       if (lane == 0) S.valid[n % kValidRing][u] = bits;
     }
     warp_arrive(&S.rows_full[slot]);
-    x = y;
-    y = z;
   }
 }
 
@@ -541,8 +534,9 @@ __device__ __forceinline__ void decode_blocks(Smem& S, RowStream<kSplits> rows, 
       const bool mine = n < n0 + r.nblk;
       const uint32_t free = ((n >> 1) & 1) ^ 1;
       if (q_pending) {
-        // Q's tile is free once S of the row before's last block has read it
-        if (!(ok = wait_warp(&S.s_full[(n0 - 1) & 1], ((n0 - 1) >> 1) & 1, a.status, 59))) break;
+        // Q's tile is free once S of the row before's last block has read it.  (A barrier
+        // of its own: this group may not have seen the S before on that block's.)
+        if (!(ok = wait_warp(&S.q_idle, (busy - 1) & 1, a.status, 59))) break;
         load_q(rows.t);
       }
       if (mine) {
@@ -555,16 +549,19 @@ __device__ __forceinline__ void decode_blocks(Smem& S, RowStream<kSplits> rows, 
         warp_arrive_first(&S.k_full[g], first);
         if (stamp) tstamp(a.trace, rank, 0, n);
       }
+      // The output of the row before has left the values' stage.  Waited for in every
+      // row, and in one without a block of this parity before its Q is handed over: a
+      // parity tells two phases apart, not three, and such a row could end without this
+      // group.
+      const bool idle_wait = first_in_row && busy > 0;
+      if (idle_wait && !mine && !(ok = wait_warp(&S.v_idle[g], (busy - 1) & 1, a.status, 60))) break;
       if (q_pending) {
         q_landed();
         q_pending = false;
       }
       const bool more = mine && comes(n + 2);
       if (more && !(ok = load_keys(n + 2))) break;
-      // the output of the row before has left the values' stage (waited for in every
-      // row, also one without a block of this parity: a parity tells two phases apart,
-      // not three)
-      if (first_in_row && busy > 0 && !(ok = wait_warp(&S.v_idle[g], (busy - 1) & 1, a.status, 60))) break;
+      if (idle_wait && mine && !(ok = wait_warp(&S.v_idle[g], (busy - 1) & 1, a.status, 60))) break;
       first_in_row = false;
       if (mine) {
         // the values' stage is free once P V of block n-2 has read it
@@ -757,6 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_c
     mbar_init(&S.q_full, 2 * 2 * kDecWarps);
     mbar_init(&S.o_free, 2 * kSmWarps);
     mbar_init(&S.drained, 1);
+    mbar_init(&S.q_idle, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.k_full[i], 2 * kDecWarps);
       mbar_init(&S.v_full[i], 2 * kDecWarps);
@@ -792,8 +790,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_c
     __syncwarp();
     cluster_arrive();
     if (rank == 0) wait_warp(&S.drained, 0, a.status, 46);
-  } else if (warp == kRowWarp) {
-    resolve_rows<kSplits>(S, rows, rank);
+  } else if (warp >= kRowWarp) {
+    resolve_rows<kSplits>(S, rows, rank, warp - kRowWarp);
     cluster_wait();
     cluster_arrive();
   } else if (warp >= kDecWarp0) {

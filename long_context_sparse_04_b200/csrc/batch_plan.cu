@@ -5,13 +5,15 @@
 // Optimization": paged caches).  The rule is stated at dsa_batch_plan in
 // include/dsa.h.
 //
-// Everything follows from four prefix sums over the requests: pages handed back,
-// pages and rows asked for (the admission), and pages and rows granted.  Every CTA
-// computes them for itself, keeps the three that the rest needs in shared memory, and
-// writes its share of the rows, table entries and pages; a binary search in shared
-// memory gives a row's request.  One CTA plans a decoding batch; a chunked prefill of
-// 131,072 rows takes 128 (redoing the sums costs them nothing: one CTA after another
-// would wait for them all the same, and a cluster, which could share them, is 8 CTAs).
+// Everything follows from five prefix sums over the requests: pages handed back and
+// pages and rows asked for (the admission) in one scan, pages and rows granted in
+// another.  Every CTA computes them for itself, keeps the three that the rest needs in
+// shared memory, and writes its share of the rows, table entries and pages; a binary
+// search in shared memory gives a row's request.  One CTA plans a decoding batch; a
+// chunked prefill of 131,072 rows takes 128 (redoing the sums costs them nothing: one
+// CTA after another would wait for them all the same, and a cluster, which could share
+// them, is 8 CTAs).  What bounds it is latency: the launch, two loads in a chain, the
+// scans' barriers, the searches.
 // Lengths and the free count, which may be updated in place, are written by the CTA
 // that finishes last, when every CTA has read them; free-list entries read (below the
 // old count) and written (at or above it) never meet, nor do table entries read (pages
@@ -23,7 +25,10 @@
 namespace dsa {
 namespace {
 
-constexpr int kThreads = 1024;
+// Threads per CTA: few for a decoding batch, whose two scans are a chain of barriers (256
+// requests: 6.5 us a plan with 256 threads, 7.8 with 1,024 and three scans; 4,096
+// requests and 131,072 rows: 18.0).
+constexpr int kFew = 256, kMany = 1024;
 constexpr int kMaxSeqs = 16384;        // three int32 prefix arrays in shared memory
 
 // One request as the rule sees it.
@@ -73,34 +78,57 @@ __device__ __forceinline__ Request request_of(const PlanArgs& a, int b, const Le
   return r;
 }
 
-// Exclusive prefix of (x, y) over the block's threads; totals in tx, ty.
-__device__ __forceinline__ void block_scan2(int64_t& x, int64_t& y, int64_t& tx, int64_t& ty,
-                                            int64_t (*part)[kThreads / 32]) {
+// Exclusive prefixes of N values over the block's threads, and their totals.
+template <int kThreads, int N>
+__device__ __forceinline__ void block_scan(int64_t (&x)[N], int64_t (&total)[N], int64_t (*part)[kThreads / 32]) {
+  constexpr int kWarps = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t x0 = x, y0 = y;
+  int64_t own[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) own[k] = x[k];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
-    if (lane >= o) { x += u; y += v; }
-  }
-  if (lane == 31) { part[0][warp] = x; part[1][warp] = y; }
-  __syncthreads();
-  if (warp == 0) {
-    int64_t u = part[0][lane], v = part[1][lane];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t p = __shfl_up_sync(0xffffffffu, u, o), q = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) { u += p; v += q; }
+    for (int k = 0; k < N; ++k) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, x[k], o);
+      if (lane >= o) x[k] += u;
     }
-    part[0][lane] = u;
-    part[1][lane] = v;
+  }
+  if (lane == 31) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) part[k][warp] = x[k];
   }
   __syncthreads();
-  x += (warp ? part[0][warp - 1] : 0) - x0;
-  y += (warp ? part[1][warp - 1] : 0) - y0;
-  tx = part[0][31];
-  ty = part[1][31];
-  __syncthreads();
+  if (kWarps > 8) {                             // warp k scans the warps' sums of value k
+    if (warp < N) {
+      int64_t u = lane < kWarps ? part[warp][lane] : 0;
+#pragma unroll
+      for (int o = 1; o < kWarps; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, u, o);
+        if (lane >= o) u += v;
+      }
+      if (lane < kWarps) part[warp][lane] = u;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      x[k] += (warp > 0 ? part[k][warp - 1] : 0) - own[k];
+      total[k] = part[k][kWarps - 1];
+    }
+  } else {                                      // every warp adds them up
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      int64_t before = 0, all = 0;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        const int64_t p = part[k][i];
+        before += i < warp ? p : 0;
+        all += p;
+      }
+      x[k] += before - own[k];
+      total[k] = all;
+    }
+  }
 }
 
 // Largest b of [0, n) with start[b] <= i, for start[0] = 0 <= i < start[n]: the
@@ -122,9 +150,10 @@ struct PlanShared {
 };
 static_assert(sizeof(PlanShared) <= sizeof(DeviceStatus::pad), "status block");
 
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads, 1) batch_plan_kernel(const __grid_constant__ PlanArgs a) {
   extern __shared__ int32_t sm[];
-  __shared__ int64_t part[2][kThreads / 32];
+  __shared__ int64_t part[5][kThreads / 32];  // of the first scan, of the second
   __shared__ int s_worst, s_refused, s_last;
   const int B = a.num_seqs, tid = threadIdx.x;
   int32_t* tok_start = sm;                  // rows granted before request b, [B + 1]
@@ -148,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) batch_plan_kernel(const __grid_co
   // what each request asks for or hands back
   const int per = (B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
-  int64_t give = 0, rows = 0, need = 0, zero = 0, gives, ignore0, ignore1;
+  int64_t asked[3] = {0, 0, 0}, asked_all[3];  // pages handed back, pages and rows asked for
   int refused = 0;
   constexpr int kBatch = 4;                 // loads of as many requests at a time
   for (int bb = b0; bb < b1; bb += kBatch) {
@@ -164,20 +193,19 @@ __global__ void __launch_bounds__(kThreads, 1) batch_plan_kernel(const __grid_co
       tok_start[b] = (int32_t)r.rows();
       pg_start[b] = r.need;
       give_start[b] = r.give;
-      rows += r.rows();
-      need += r.need;
-      give += r.give;
+      asked[0] += r.give;
+      asked[1] += r.need;
+      asked[2] += r.rows();
       if (r.err) {
         atomicMax(&s_worst, INT_MAX - (b * 8 + r.err));
         ++refused;
       }
     }
   }
-  block_scan2(give, zero, gives, ignore0, part);
-  block_scan2(need, rows, ignore0, ignore1, part);
-  const int64_t have = F + gives;
+  block_scan<kThreads>(asked, asked_all, part);
+  const int64_t gives = asked_all[0], have = F + gives;
   // the admission: inclusive sums of pages and rows over every request that could run
-  int64_t my_rows = 0, my_pages = 0;
+  int64_t give = asked[0], need = asked[1], rows = asked[2], granted[2] = {0, 0}, granted_all[2];
   for (int b = b0; b < b1; ++b) {
     const int32_t n = tok_start[b], p = pg_start[b], g = give_start[b];
     need += p;
@@ -187,20 +215,20 @@ __global__ void __launch_bounds__(kThreads, 1) batch_plan_kernel(const __grid_co
       tok_start[b] = pg_start[b] = 0;
       ++refused;
     }
-    my_rows += go ? n : 0;
-    my_pages += go ? p : 0;
+    granted[0] += go ? n : 0;
+    granted[1] += go ? p : 0;
     give_start[b] = (int32_t)give;
     give += g;
   }
   if (refused) atomicAdd(&s_refused, refused);
-  int64_t total, taken;
-  block_scan2(my_rows, my_pages, total, taken, part);
+  block_scan<kThreads>(granted, granted_all, part + 3);
+  const int64_t total = granted_all[0], taken = granted_all[1];
   for (int b = b0; b < b1; ++b) {
     const int32_t n = tok_start[b], p = pg_start[b];
-    tok_start[b] = (int32_t)my_rows;
-    pg_start[b] = (int32_t)my_pages;
-    my_rows += n;
-    my_pages += p;
+    tok_start[b] = (int32_t)granted[0];
+    pg_start[b] = (int32_t)granted[1];
+    granted[0] += n;
+    granted[1] += p;
   }
   if (tid == 0) {
     tok_start[B] = (int32_t)total;
@@ -296,12 +324,17 @@ int batch_plan_max_seqs() { return kMaxSeqs; }
 dsa_status launch_batch_plan(const PlanArgs& a, cudaStream_t stream) {
   const size_t smem_max = (size_t)3 * (kMaxSeqs + 1) * sizeof(int32_t);
   static std::atomic<bool> attr[kMaxDevices] = {};
-  if (dsa_status st = set_smem_limit_once(reinterpret_cast<const void*>(batch_plan_kernel), smem_max, attr))
+  if (dsa_status st = set_smem_limit_once(reinterpret_cast<const void*>(batch_plan_kernel<kMany>), smem_max, attr))
     return st;
-  // a CTA for every kThreads rows, at most one per SM
-  const int64_t want = ((int64_t)a.p.max_tokens + kThreads - 1) / kThreads;
-  const int most = device_sm_count(), ctas = want < 1 ? 1 : want < most ? (int)want : most;
-  batch_plan_kernel<<<ctas, kThreads, (size_t)3 * (a.num_seqs + 1) * sizeof(int32_t), stream>>>(a);
+  const size_t smem = (size_t)3 * (a.num_seqs + 1) * sizeof(int32_t);
+  if (a.num_seqs <= 2 * kFew && a.p.max_tokens <= 8 * kFew) {
+    batch_plan_kernel<kFew><<<1, kFew, smem, stream>>>(a);
+  } else {
+    // a CTA for every kMany rows, at most one per SM
+    const int64_t want = ((int64_t)a.p.max_tokens + kMany - 1) / kMany;
+    const int most = device_sm_count(), ctas = want < 1 ? 1 : want < most ? (int)want : most;
+    batch_plan_kernel<kMany><<<ctas, kMany, smem, stream>>>(a);
+  }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("batch plan launch failed: %s", cudaGetErrorString(e));

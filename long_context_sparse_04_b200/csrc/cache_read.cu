@@ -8,8 +8,10 @@
 //   latent_out[n] = code * scale per 16 dims, bf16   (exact), RoPE key copied
 //
 // A stream: with 4-bit latents 548 bytes in and 1,664 out per token, so writes
-// bound it.  One warp per token; a lane decodes one group of 16 dims (8 bytes of
-// codes) into 32 bytes.
+// bound it.  131,072 tokens take 59.7 us, 4.9 TB/s (a kernel that copies 218 MB of
+// such output alone ran at 5.9).  One warp per token: two tokens a warp, persistent
+// warps and a ring filled by cp.async took 70-89 us, a lane that decodes a whole group
+// of 16 dims (so that a warp's stores are every other 16 bytes) 63.6.
 #include <cuda_fp8.h>
 
 #include "dsa_int4.cuh"

@@ -25,7 +25,7 @@
 // both for itself straight from the packed rows: at three instructions a pair of
 // values that is cheaper than an exchange through distributed shared memory.
 //
-// Roles per CTA (864 threads):
+// Roles per CTA (896 threads):
 //   warps 0-7    softmax and output, two groups of four warps that take the blocks in
 //                turn: a block's chain (wait, tensor-memory load, maximum, weights,
 //                store) is longer than its products take, so one group would set the
@@ -38,16 +38,23 @@
 //                blocks' time ahead of their use (one block's was too little: the loads
 //                set the pace), then 16-byte stores, swizzled, of the keys' and the
 //                values' tile
-//   warp 24      tensor memory; in the pair's first CTA one thread issues the MMAs
+//   warp 24      tensor memory; in the pair's first CTA one thread issues Q K^T
 //   warps 25-26  resolve the selection to cache rows, up to four blocks ahead
-// Tiles, weights and logits have two stages each; S of block j+1 is issued before
-// P V of block j, so that the tensor cores work while the softmax of block j runs.
+//   warp 27      in the first CTA one thread issues P V
+// Tiles, weights and logits have two stages each; S of block j+1 runs before P V of
+// block j, so that the tensor cores work while the softmax of block j does.
 // Without key splits the kernel is persistent: a pair takes rows t, t + pairs, ...,
 // its blocks one stream across rows (block counter n: stage and group n % 2), so that
 // the next row's selection, rows, tiles and Q come in while this row is finished.
 //
 // Decode batches split a row's keys over 2 or 4 pairs of one cluster, which merge
 // through distributed shared memory: no scratch in global memory, no arrival order.
+//
+// Measured with 128 heads and 2,048 selected keys: 32 rows 31 us (58,000 cycles: 8,000
+// to the first tile, 16 blocks, 12,000 of merge and output) against a floor of 11.1 us
+// of tensor time; 2,048 rows 1.12 ms (1.05 PFLOP/s) on a cool card and 1.25 under its
+// power cap, floor 0.71.  A block takes about 2,000 cycles; issue slots are 62 % used:
+// the decoding and the softmax bound it, not the tensor cores (45 % active).
 #include <cudaTypedefs.h>
 
 #include "dsa_int4.cuh"
@@ -64,15 +71,15 @@ constexpr int kBlk = 64, kHalfBlk = 32;
 constexpr int kMaxKeys = 2048;
 constexpr int kMaxPairs = 4;                    // key splits of a row: 1, 2 or 4 (a cluster of 8 CTAs)
 constexpr int kSmWarps = 8, kDecWarps = 8;
-constexpr int kDecWarp0 = 8, kMmaWarp = 24, kRowWarp = 25, kRowWarps = 2;
-constexpr int kThreads = 32 * (kRowWarp + kRowWarps);
+constexpr int kDecWarp0 = 8, kMmaWarp = 24, kRowWarp = 25, kRowWarps = 2, kMmaWarp2 = 27;
+constexpr int kThreads = 32 * 28;
 constexpr int kSmThreads = 32 * kSmWarps;
 constexpr int kDecThreads = 2 * kDecWarps * 32;
 constexpr int kQChunks = kD / 64;               // 64-dim SW128 chunks: 8 latent, 1 RoPE
 constexpr uint32_t kColS = 0, kColO = 64, kTmemCols = 512;
 // Blocks in the ring of resolved rows, and in that of their validity bits: block n's are
-// read by the softmax after S of block n, and resolving block n + 10 waits for weights
-// that come after that read (rows n + 6 loaded, hence S of block n + 2, P V of block n).
+// read by the softmax before its weights are stored, and resolving block n + 10 waits for
+// those (rows n + 6 loaded, keys n + 4 stored, S of block n + 2 done, weights n stored).
 constexpr int kRowRing = 4, kValidRing = 16;
 // polls of a bounded wait (20 ms at least; real waits take microseconds)
 constexpr uint32_t kWaitPolls = 1u << 20;
@@ -210,6 +217,10 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint16_t mask) {
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)), "h"(mask) : "memory");
 }
+// The same on `bar` of this CTA alone.
+__device__ __forceinline__ void mma_commit_own(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 // Bounded wait; on time-out records DSA_ERR_TIMEOUT (detail = site) and returns
 // false.  Written out so that a barrier already complete costs two instructions:
 // every warp passes two to four of them a block.
@@ -256,64 +267,74 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// ---------------------------------------------------------------- MMA issue (first CTA, one thread)
+// ---------------------------------------------------------------- MMA issue (first CTA)
+// One thread for each product: the 36 MMAs of S take an issuing warp, which shares its
+// scheduler with six others, about as long as the tensor cores, so a wait for weights
+// must not stand before them (148 rows: 85.2 us with two threads, 86.2 with one; the
+// issuing loop rolled up, which costs a few more instructions an MMA, took it to 114).
+// A byte offset within a tile adds offset >> 4 to a descriptor's address field.
 template <int kSplits>
-__device__ __forceinline__ void issue_products(Smem& S, RowStream<kSplits> rows, uint32_t tmem, uint16_t mask) {
+__device__ __forceinline__ void issue_logits(Smem& S, RowStream<kSplits> rows, uint32_t tmem, uint16_t mask) {
   const MlaArgs& a = rows.a;
   DeviceStatus* status = a.status;
-  constexpr uint32_t idesc_s = idesc_bf16(kBlk, false);
-  constexpr uint32_t idesc_pv = idesc_bf16(256, true);
-  // descriptors: a byte offset within the tile adds offset >> 4 to the address field
-  const uint64_t qd = sdesc_sw128(smem_u32(S.q), 16, 1024), pd = sdesc_sw128(smem_u32(S.p), 16, 1024);
-  const uint64_t kd0 = sdesc_sw128(smem_u32(S.k[0]), 16, 1024);
-  const uint64_t vd0 = sdesc_sw128(smem_u32(S.v[0]), kBlk * 128, 1024);
+  constexpr uint32_t idesc = idesc_bf16(kBlk, false);
+  const uint64_t qd = sdesc_sw128(smem_u32(S.q), 16, 1024), kd0 = sdesc_sw128(smem_u32(S.k[0]), 16, 1024);
   Row r;
   bool ok = true;
   uint32_t busy = 0;                              // rows with keys so far
   for (int n0 = 0; ok && rows.next_busy(r); n0 += r.nblk, ++busy) {
     ok = wait_local(&S.q_full, busy & 1, status, 41);
-    for (int j = 0; ok && j <= r.nblk; ++j) {
-      if (j < r.nblk) {
-        const int n = n0 + j, b = n & 1;
-        // (S of block n-2 has been read: P V of that block waited for its weights)
-        if (!(ok = wait_local(&S.k_full[b], (n >> 1) & 1, status, 42))) break;
-        tc_fence_after();
-        const uint64_t kd = kd0 + (uint64_t)(b * (sizeof(S.k[0]) >> 4));
-        const uint32_t d = tmem + kColS + b * 32;
+    for (int j = 0; ok && j < r.nblk; ++j) {
+      const int n = n0 + j, b = n & 1;
+      // the keys are there, and S of block n-2 has been read: its weights are there
+      ok = wait_local(&S.p_full[b], ((n >> 1) & 1) ^ 1, status, 43) && wait_local(&S.k_full[b], (n >> 1) & 1, status, 42);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t kd = kd0 + (uint64_t)(b * (sizeof(S.k[0]) >> 4));
+      const uint32_t d = tmem + kColS + b * 32;
 #pragma unroll
-        for (int ch = 0; ch < kQChunks; ++ch)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_bf16_pair(d, qd + (ch * kHc * 128 + 32 * kk >> 4), kd + (ch * kHalfBlk * 128 + 32 * kk >> 4), idesc_s,
-                          (ch | kk) != 0);
-        mma_commit_pair(&S.s_full[b], mask);
-        if (kSplits == 1 && j + 1 == r.nblk) mma_commit_pair(&S.q_idle, mask);
-        tstamp(a.trace, 0, 2, n);
-      }
-      if (j >= 1) {
-        const int n = n0 + j - 1, b = n & 1;
-        ok = wait_local(&S.v_full[b], (n >> 1) & 1, status, 44) && wait_local(&S.p_full[b], (n >> 1) & 1, status, 45);
-        // the row before has been read out of the accumulator
-        if (j == 1 && busy > 0) ok = ok && wait_local(&S.o_free, (busy - 1) & 1, status, 58);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t vd = vd0 + (uint64_t)(b * (sizeof(S.v[0]) >> 4));
+      for (int ch = 0; ch < kQChunks; ++ch)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            mma_bf16_pair(tmem + kColO + h * 128, pd + b * (sizeof(S.p[0]) >> 4) + (32 * kk >> 4),
-                          vd + (h * 2 * kBlk * 128 + kk * 16 * 128 >> 4), idesc_pv, ((j - 1) | kk) != 0);
-        mma_commit_pair(&S.pv_done[b], mask);
-        tstamp(a.trace, 0, 3, n);
-      }
+          mma_bf16_pair(d, qd + (ch * kHc * 128 + 32 * kk >> 4), kd + (ch * kHalfBlk * 128 + 32 * kk >> 4), idesc, (ch | kk) != 0);
+      mma_commit_pair(&S.s_full[b], mask);
+      if (kSplits == 1 && j + 1 == r.nblk) mma_commit_pair(&S.q_idle, mask);
+      tstamp(a.trace, 0, 2, n);
     }
   }
-  // the last row's arrivals from the other CTA are in, and every product issued is done,
-  // before the pair's shared and tensor memory go
+  mma_commit_own(&S.drained);
+}
+template <int kSplits>
+__device__ __forceinline__ void issue_outputs(Smem& S, RowStream<kSplits> rows, uint32_t tmem, uint16_t mask) {
+  const MlaArgs& a = rows.a;
+  DeviceStatus* status = a.status;
+  constexpr uint32_t idesc = idesc_bf16(256, true);
+  const uint64_t pd0 = sdesc_sw128(smem_u32(S.p), 16, 1024), vd0 = sdesc_sw128(smem_u32(S.v[0]), kBlk * 128, 1024);
+  Row r;
+  bool ok = true;
+  uint32_t busy = 0;
+  for (int n0 = 0; ok && rows.next_busy(r); n0 += r.nblk, ++busy) {
+    for (int j = 0; ok && j < r.nblk; ++j) {
+      const int n = n0 + j, b = n & 1;
+      ok = wait_local(&S.v_full[b], (n >> 1) & 1, status, 44) && wait_local(&S.p_full[b], (n >> 1) & 1, status, 45);
+      // the row before has been read out of the accumulator
+      if (j == 0 && busy > 0) ok = ok && wait_local(&S.o_free, (busy - 1) & 1, status, 58);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t vd = vd0 + (uint64_t)(b * (sizeof(S.v[0]) >> 4)), pd = pd0 + (uint64_t)(b * (sizeof(S.p[0]) >> 4));
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          mma_bf16_pair(tmem + kColO + h * 128, pd + (32 * kk >> 4), vd + (h * 2 * kBlk * 128 + kk * 16 * 128 >> 4), idesc,
+                        (j | kk) != 0);
+      mma_commit_pair(&S.pv_done[b], mask);
+      tstamp(a.trace, 0, 3, n);
+    }
+  }
+  // the last row's arrivals from the other CTA are in
   if (kSplits == 1 && ok && busy > 0) wait_local(&S.o_free, (busy - 1) & 1, status, 58);
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&S.drained))
-               : "memory");
+  mma_commit_own(&S.drained);
 }
 
 // ---------------------------------------------------------------- the selection
@@ -634,6 +655,9 @@ struct Softmax {
                                         uint32_t rank, uint32_t first) {
     const int l = threadIdx.x & 127, half = l >> 6, hl = l & 63;
     const uint32_t phase = (n >> 1) & 1;
+    // the weights' tile is free once P V of block n-2 has read it (waited for here, where
+    // the group waits for its logits anyway)
+    dead = dead || !wait_local(&S.pv_done[g], phase ^ 1, a.status, 51);
     dead = dead || !wait_local(&S.s_full[g], phase, a.status, 49);
     tc_fence_after();
     if (l == 0 && a.trace != nullptr) tstamp(a.trace, rank, 4, n);
@@ -693,8 +717,6 @@ struct Softmax {
       sum *= m == -INFINITY ? 0.f : exp2f(m - m_now);
       m = m_now;
     }
-    // (the weights' tile is free: P V of block j-2 was issued before S of this block,
-    // and a commit covers all that was issued before it)
     // p = 2^(c s - m); while no key of the head has been visible m counts as 0
     const float mu = (m == -INFINITY) ? 0.f : -m;
     const uint64_t c2 = pair_f32(c, c), mu2 = pair_f32(mu, mu);
@@ -753,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_c
   if (threadIdx.x == 0) {
     mbar_init(&S.q_full, 2 * 2 * kDecWarps);
     mbar_init(&S.o_free, 2 * kSmWarps);
-    mbar_init(&S.drained, 1);
+    mbar_init(&S.drained, 2);
     mbar_init(&S.q_idle, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.k_full[i], 2 * kDecWarps);
@@ -784,11 +806,15 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_c
   RowStream<kSplits> rows(a, blockIdx.x / (2 * kSplits), kSplits > 1 ? a.num_rows : (int)gridDim.x / 2, sp);
   using Mg = Merge<kSplits>;
 
-  if (warp == kMmaWarp) {
+  if (warp == kMmaWarp || warp == kMmaWarp2) {
     cluster_wait();
-    if (rank == 0 && elect_one()) issue_products<kSplits>(S, rows, tmem, (uint16_t)(3u << first));
+    if (rank == 0 && elect_one()) {
+      if (warp == kMmaWarp) issue_logits<kSplits>(S, rows, tmem, (uint16_t)(3u << first));
+      else issue_outputs<kSplits>(S, rows, tmem, (uint16_t)(3u << first));
+    }
     __syncwarp();
     cluster_arrive();
+    // every product issued is done before the pair's shared and tensor memory go
     if (rank == 0) wait_warp(&S.drained, 0, a.status, 46);
   } else if (warp >= kRowWarp) {
     resolve_rows<kSplits>(S, rows, rank, warp - kRowWarp);

@@ -54,9 +54,10 @@ __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t u) {
 __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) { return *reinterpret_cast<uint32_t*>(&v); }
 __device__ __forceinline__ ScalePair scale_pair(uint32_t b) {
   ScalePair p;
-  // 0x7780 = 2^112, 0xC308 = -136
-  p.s = __hmul2(as_bf162((b << 4) * 0x00010001u), as_bf162(0x77807780u));
-  p.off = __hmul2(p.s, as_bf162(0xC308C308u));
+  // 0x7780 = 2^112, 0xFB08 = -136 * 2^112
+  const __nv_bfloat162 x = as_bf162((b << 4) * 0x00010001u);
+  p.s = __hmul2(x, as_bf162(0x77807780u));
+  p.off = __hmul2(x, as_bf162(0xFB08FB08u));
   return p;
 }
 // Eight dims of one word as four bf16x2, in order.  (The and-xor is written as one

@@ -50,11 +50,12 @@
 // Decode batches split a row's keys over 2 or 4 pairs of one cluster, which merge
 // through distributed shared memory: no scratch in global memory, no arrival order.
 //
-// Measured with 128 heads and 2,048 selected keys: 32 rows 31 us (58,000 cycles: 8,000
+// Measured with 128 heads and 2,048 selected keys: 32 rows 30 us (56,000 cycles: 8,000
 // to the first tile, 16 blocks, 12,000 of merge and output) against a floor of 11.1 us
-// of tensor time; 2,048 rows 1.12 ms (1.05 PFLOP/s) on a cool card and 1.25 under its
-// power cap, floor 0.71.  A block takes about 2,000 cycles; issue slots are 62 % used:
-// the decoding and the softmax bound it, not the tensor cores (45 % active).
+// of tensor time; 2,048 rows 1.11 ms (1.05 PFLOP/s) on a cool card and 1.25 under its
+// power cap, floor 0.71.  A block takes about 2,000 cycles: what a decoding group needs
+// for its two tiles of two blocks, waits and arrivals included, at 8 cycles an
+// instruction (issue slots 62 % used, tensor pipe 45 %).
 #include <cudaTypedefs.h>
 
 #include "dsa_int4.cuh"
@@ -256,11 +257,8 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Device
 // local window (mapa of the base, taken once).
 __device__ __forceinline__ void warp_arrive_first(uint64_t* bar, uint32_t first) {
   __syncwarp();
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .u32 l;\n\t"
-      "mov.u32 l, %%laneid;\n\t"
-      "setp.eq.u32 p, l, 0;\n\t"
-      "@p mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar) + first) : "memory");
+  if ((threadIdx.x & 31) == 0)
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(smem_u32(bar) + first) : "memory");
 }
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();

@@ -34,6 +34,7 @@ namespace dsa {
 namespace {
 
 constexpr int kWarpsPerCta = 8;     // tokens per CTA
+constexpr int kPackedWarps = 4;     // the same for packed rows
 constexpr int kMaxKeyChunks = 4;    // float4 per lane: d_I <= 4 * 32 * 4 = 512
 constexpr int kLatGroup = 3;        // 16-byte latent chunks per lane in flight (1152 B rows: one group)
 
@@ -292,11 +293,12 @@ cache_append_kernel(const AppendArgs a) {
 }
 
 // Packed rows.  A lane quantises whole groups of 16 latent dims (d_c = 512: one each),
-// so a group's maximum needs no exchange.  65,536 tokens take 39 us against a floor of
+// so a group's maximum needs no exchange.  65,536 tokens take 37 us against a floor of
 // 22 us for their 146 MB: what bounds it is the integer pipe (unpacking, packing and
-// comparing; a warp instruction takes it two cycles): fp32 pairs and bf16 pair maxima
-// took it from 42.4 to 39.2.  Persistent warps with the next token's loads in flight
-// measured the same, four CTAs an SM without the spills 41.3.
+// comparing; a warp instruction takes it two cycles).  fp32 pairs and bf16 pair maxima
+// took it from 42.4 to 39.2, CTAs of four warps instead of eight to 37.2.  Persistent
+// warps with the next token's loads in flight measured the same; 32 warps an SM, which
+// spill nothing, 41.3.
 struct Token {
   float4 key;              // this lane's first key chunk (d_I > 128: the others are loaded late)
   uint4 lat[2], rope;      // its group of 16 dims, its piece of the RoPE key
@@ -389,11 +391,11 @@ __device__ __forceinline__ void store_token(const AppendArgs& a, int64_t n, cons
 }
 
 template <bool kSlots>
-__global__ void __launch_bounds__(kWarpsPerCta * 32, 5)
+__global__ void __launch_bounds__(kPackedWarps * 32, 10)
 cache_append_int4_kernel(const __grid_constant__ AppendArgs a) {
   pdl_launch_dependents();
   trace_kernel(a.status, DSA_KERNEL_CACHE_APPEND);
-  const int64_t n = (int64_t)blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
+  const int64_t n = (int64_t)blockIdx.x * kPackedWarps + (threadIdx.x >> 5);
   if (n >= a.n_new) return;
   Token x;
   load_token<kSlots>(a, n, x);
@@ -404,10 +406,11 @@ cache_append_int4_kernel(const __grid_constant__ AppendArgs a) {
 
 dsa_status launch_cache_append(const AppendArgs& a, cudaStream_t stream) {
   if (a.n_new == 0) return DSA_OK;
-  const unsigned grid = (unsigned)(((int64_t)a.n_new + kWarpsPerCta - 1) / kWarpsPerCta);
+  const int warps = a.int4 ? kPackedWarps : kWarpsPerCta;
+  const unsigned grid = (unsigned)(((int64_t)a.n_new + warps - 1) / warps);
   void (*kernel)(AppendArgs) = a.slot ? cache_append_kernel<true> : cache_append_kernel<false>;
   if (a.int4) kernel = a.slot ? cache_append_int4_kernel<true> : cache_append_int4_kernel<false>;
-  kernel<<<grid, kWarpsPerCta * 32, 0, stream>>>(a);
+  kernel<<<grid, warps * 32, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("cache append launch failed: %s", cudaGetErrorString(e));

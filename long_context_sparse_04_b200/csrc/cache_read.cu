@@ -8,10 +8,10 @@
 //   latent_out[n] = code * scale per 16 dims, bf16   (exact), RoPE key copied
 //
 // A stream: with 4-bit latents 548 bytes in and 1,664 out per token, so writes
-// bound it.  131,072 tokens take 59.7 us, 4.9 TB/s (a kernel that copies 218 MB of
-// such output alone ran at 5.9).  One warp per token: two tokens a warp, persistent
-// warps and a ring filled by cp.async took 70-89 us, a lane that decodes a whole group
-// of 16 dims (so that a warp's stores are every other 16 bytes) 63.6.
+// bound it.  131,072 tokens take 55.7 us, 5.2 TB/s (a kernel that copies 218 MB of
+// such output alone ran at 5.9).  One warp per token, CTAs of four, fourteen an SM:
+// eight warps a CTA took 57.6 us, sixteen 61.7, two 71; two tokens a warp, persistent
+// warps and a ring filled by cp.async 70-89; 32-byte stores 66.7.
 #include <cuda_fp8.h>
 
 #include "dsa_int4.cuh"
@@ -20,7 +20,7 @@
 namespace dsa {
 namespace {
 
-constexpr int kWarpsPerCta = 8;
+constexpr int kWarpsPerCta = 4;
 
 __device__ __forceinline__ float4 e4m3x4_to_f32(uint32_t w, float s) {
   float f[4];
@@ -47,7 +47,7 @@ __device__ __forceinline__ int64_t slot_of(const ReadArgs& a, int64_t n) {
 // Packed rows, one warp per token.  A lane decodes words of eight dims, 32 apart, so
 // that a warp's stores are whole lines, and all of a token's loads are issued before
 // its first store (d_c <= 512: two words a lane).
-__global__ void __launch_bounds__(kWarpsPerCta * 32) cache_read_int4_kernel(const __grid_constant__ ReadArgs a) {
+__global__ void __launch_bounds__(kWarpsPerCta * 32, 14) cache_read_int4_kernel(const __grid_constant__ ReadArgs a) {
   pdl_launch_dependents();
   trace_kernel(a.status, DSA_KERNEL_CACHE_READ);
   const int lane = threadIdx.x & 31;

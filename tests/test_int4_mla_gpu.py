@@ -430,3 +430,21 @@ def test_first_call_of_a_process_is_captured(N, T):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     p = subprocess.run([sys.executable, "-c", FIRST.format(root=root, T=T)], cwd=root, capture_output=True, text=True, timeout=300)
     assert p.returncode == 0, p.stderr[-2000:]
+
+
+@pytest.mark.parametrize("blocks", [1, 2, 3, 4, 5])
+def test_repeated_calls_agree(N, blocks):
+    """Rows of the same number of blocks (and neighbours of others), call after call: a
+    pair's tiles change rows at every parity."""
+    import torch
+    rng = np.random.default_rng(blocks)
+    k = np.where(rng.random(260) < 0.8, 64 * blocks - rng.integers(0, 64, 260), rng.integers(0, 400, 260))
+    c = Case(N, [int(x) for x in k], H=128, topk=512, seed=blocks, seqs=[int(x) for x in rng.integers(0, 5, 260)]).build().call()
+    c.check(rows=range(0, 260, 13))
+    out, lse = c.d["out"].clone(), c.d["lse"].clone()
+    for _ in range(40):
+        c.d["out"].fill_(7.0)
+        c.d["out"][c.T:] = 55.0
+        c.call()
+        assert torch.equal(c.d["out"], out) and torch.equal(c.d["lse"], lse)
+    assert c.status() == (0, -1)

@@ -223,10 +223,21 @@ __device__ __forceinline__ void mma_commit_own(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 // Bounded wait; on time-out records DSA_ERR_TIMEOUT (detail = site) and returns
-// false.  Written out so that a barrier already complete costs two instructions:
-// every warp passes two to four of them a block.
+// false.  Written out so that a barrier already complete costs few instructions: every
+// warp passes two to four of them a block.  kShort: a first try apart from the loop,
+// cheaper where barriers are mostly complete.  With key splits that is so (32 rows: 29.8
+// against 30.3 us); in the persistent kernel, whose warps wait more, it was slower (16
+// heads: 27.5 against 26.6 us).
+template <bool kShort>
 __device__ __forceinline__ bool wait_local(uint64_t* bar, uint32_t parity, DeviceStatus* st, int site) {
   uint32_t ok;
+  if (kShort) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    if (ok) return true;
+  }
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
       "mov.u32 n, %3;\n"
@@ -243,8 +254,9 @@ __device__ __forceinline__ bool wait_local(uint64_t* bar, uint32_t parity, Devic
   return ok != 0;
 }
 // The same, agreed on by the warp (its lanes go on or leave together).
+template <bool kShort>
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, DeviceStatus* st, int site) {
-  return __all_sync(0xffffffffu, wait_local(bar, parity, st, site));
+  return __all_sync(0xffffffffu, wait_local<kShort>(bar, parity, st, site));
 }
 // One arrival per warp on a barrier of the pair's first CTA.  What it announces
 // lies in the arriving CTA's own shared or tensor memory and is read by the tensor
@@ -281,11 +293,11 @@ __device__ __forceinline__ void issue_logits(Smem& S, RowStream<kSplits> rows, u
   bool ok = true;
   uint32_t busy = 0;                              // rows with keys so far
   for (int n0 = 0; ok && rows.next_busy(r); n0 += r.nblk, ++busy) {
-    ok = wait_local(&S.q_full, busy & 1, status, 41);
+    ok = wait_local<(kSplits > 1)>(&S.q_full, busy & 1, status, 41);
     for (int j = 0; ok && j < r.nblk; ++j) {
       const int n = n0 + j, b = n & 1;
       // the keys are there, and S of block n-2 has been read: its weights are there
-      ok = wait_local(&S.p_full[b], ((n >> 1) & 1) ^ 1, status, 43) && wait_local(&S.k_full[b], (n >> 1) & 1, status, 42);
+      ok = wait_local<(kSplits > 1)>(&S.p_full[b], ((n >> 1) & 1) ^ 1, status, 43) && wait_local<(kSplits > 1)>(&S.k_full[b], (n >> 1) & 1, status, 42);
       if (!ok) break;
       tc_fence_after();
       const uint64_t kd = kd0 + (uint64_t)(b * (sizeof(S.k[0]) >> 4));
@@ -314,9 +326,9 @@ __device__ __forceinline__ void issue_outputs(Smem& S, RowStream<kSplits> rows, 
   for (int n0 = 0; ok && rows.next_busy(r); n0 += r.nblk, ++busy) {
     for (int j = 0; ok && j < r.nblk; ++j) {
       const int n = n0 + j, b = n & 1;
-      ok = wait_local(&S.v_full[b], (n >> 1) & 1, status, 44) && wait_local(&S.p_full[b], (n >> 1) & 1, status, 45);
+      ok = wait_local<(kSplits > 1)>(&S.v_full[b], (n >> 1) & 1, status, 44) && wait_local<(kSplits > 1)>(&S.p_full[b], (n >> 1) & 1, status, 45);
       // the row before has been read out of the accumulator
-      if (j == 0 && busy > 0) ok = ok && wait_local(&S.o_free, (busy - 1) & 1, status, 58);
+      if (j == 0 && busy > 0) ok = ok && wait_local<(kSplits > 1)>(&S.o_free, (busy - 1) & 1, status, 58);
       if (!ok) break;
       tc_fence_after();
       const uint64_t vd = vd0 + (uint64_t)(b * (sizeof(S.v[0]) >> 4)), pd = pd0 + (uint64_t)(b * (sizeof(S.p[0]) >> 4));
@@ -331,7 +343,7 @@ __device__ __forceinline__ void issue_outputs(Smem& S, RowStream<kSplits> rows, 
     }
   }
   // the last row's arrivals from the other CTA are in
-  if (kSplits == 1 && ok && busy > 0) wait_local(&S.o_free, (busy - 1) & 1, status, 58);
+  if (kSplits == 1 && ok && busy > 0) wait_local<(kSplits > 1)>(&S.o_free, (busy - 1) & 1, status, 58);
   mma_commit_own(&S.drained);
 }
 
@@ -414,7 +426,7 @@ __device__ __forceinline__ void resolve_rows(Smem& S, RowStream<kSplits> rows, u
     }
     positions();
     const int slot = n % kRowRing;
-    if (!wait_warp(&S.rows_free[slot], (n / kRowRing & 1) ^ 1, a.status, 53)) break;
+    if (!wait_warp<(kSplits > 1)>(&S.rows_free[slot], (n / kRowRing & 1) ^ 1, a.status, 53)) break;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       int64_t row = (int64_t)e[u] + off[u];
@@ -499,7 +511,7 @@ __device__ __forceinline__ void decode_blocks(Smem& S, RowStream<kSplits> rows, 
   int v_row = -1;
   const auto load_keys = [&](int n) {
     const int slot = n % kRowRing;
-    if (!wait_warp(&S.rows_full[slot], n / kRowRing & 1, a.status, 54)) return false;
+    if (!wait_warp<(kSplits > 1)>(&S.rows_full[slot], n / kRowRing & 1, a.status, 54)) return false;
     const int k_row = S.rows[slot][own + k_key], r_row = S.rows[slot][own + (kt >> 3)];
     v_row = S.rows[slot][v_key];
     warp_arrive(&S.rows_free[slot]);
@@ -555,12 +567,12 @@ __device__ __forceinline__ void decode_blocks(Smem& S, RowStream<kSplits> rows, 
       if (q_pending) {
         // Q's tile is free once S of the row before's last block has read it.  (A barrier
         // of its own: this group may not have seen the S before on that block's.)
-        if (!(ok = wait_warp(&S.q_idle, (busy - 1) & 1, a.status, 59))) break;
+        if (!(ok = wait_warp<(kSplits > 1)>(&S.q_idle, (busy - 1) & 1, a.status, 59))) break;
         load_q(rows.t);
       }
       if (mine) {
         // the keys' stage is free once S of block n-2 has read it
-        if (!(ok = wait_warp(&S.s_full[g], free, a.status, 47))) break;
+        if (!(ok = wait_warp<(kSplits > 1)>(&S.s_full[g], free, a.status, 47))) break;
         if (stamp) tstamp(a.trace, rank, 5, n);
         ku.store(k_dst);
         *reinterpret_cast<uint4*>(r_dst) = rope;
@@ -573,18 +585,18 @@ __device__ __forceinline__ void decode_blocks(Smem& S, RowStream<kSplits> rows, 
       // parity tells two phases apart, not three, and such a row could end without this
       // group.
       const bool idle_wait = first_in_row && busy > 0;
-      if (idle_wait && !mine && !(ok = wait_warp(&S.v_idle[g], (busy - 1) & 1, a.status, 60))) break;
+      if (idle_wait && !mine && !(ok = wait_warp<(kSplits > 1)>(&S.v_idle[g], (busy - 1) & 1, a.status, 60))) break;
       if (q_pending) {
         q_landed();
         q_pending = false;
       }
       const bool more = mine && comes(n + 2);
       if (more && !(ok = load_keys(n + 2))) break;
-      if (idle_wait && mine && !(ok = wait_warp(&S.v_idle[g], (busy - 1) & 1, a.status, 60))) break;
+      if (idle_wait && mine && !(ok = wait_warp<(kSplits > 1)>(&S.v_idle[g], (busy - 1) & 1, a.status, 60))) break;
       first_in_row = false;
       if (mine) {
         // the values' stage is free once P V of block n-2 has read it
-        if (!(ok = wait_warp(&S.pv_done[g], free, a.status, 48))) break;
+        if (!(ok = wait_warp<(kSplits > 1)>(&S.pv_done[g], free, a.status, 48))) break;
         if (stamp) tstamp(a.trace, rank, 7, n);
         vu.store(v_dst);
         fence_proxy_async_smem();
@@ -649,14 +661,15 @@ struct Softmax {
 
   // Block j of the row, n = n0 + j of the pair, n % 2 = g.  A thread whose wait ran out (dead) skips its waits
   // and goes on, so that every arrival and collective access stays uniform.
+  template <int kSplits>
   __device__ __forceinline__ void block(Smem& S, const MlaArgs& a, uint32_t tmem_lane, int n, int j, int nblk, int g, float c,
                                         uint32_t rank, uint32_t first) {
     const int l = threadIdx.x & 127, half = l >> 6, hl = l & 63;
     const uint32_t phase = (n >> 1) & 1;
     // the weights' tile is free once P V of block n-2 has read it (waited for here, where
     // the group waits for its logits anyway)
-    dead = dead || !wait_local(&S.pv_done[g], phase ^ 1, a.status, 51);
-    dead = dead || !wait_local(&S.s_full[g], phase, a.status, 49);
+    dead = dead || !wait_local<(kSplits > 1)>(&S.pv_done[g], phase ^ 1, a.status, 51);
+    dead = dead || !wait_local<(kSplits > 1)>(&S.s_full[g], phase, a.status, 49);
     tc_fence_after();
     if (l == 0 && a.trace != nullptr) tstamp(a.trace, rank, 4, n);
     float s[32];
@@ -693,7 +706,7 @@ struct Softmax {
       const float alpha = need ? (m_now == -INFINITY ? 0.f : exp2f(m_now - m_new)) : 1.f;
       if (j > 0) {
         // no product is in flight: block j-1's is done, block j's waits for P below
-        dead = dead || !wait_local(&S.pv_done[g ^ 1], ((n - 1) >> 1) & 1, a.status, 50);
+        dead = dead || !wait_local<(kSplits > 1)>(&S.pv_done[g ^ 1], ((n - 1) >> 1) & 1, a.status, 50);
         tc_fence_after();
 #pragma unroll 1
         for (int cc = 0; cc < 16; ++cc) {
@@ -813,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_c
     __syncwarp();
     cluster_arrive();
     // every product issued is done before the pair's shared and tensor memory go
-    if (rank == 0) wait_warp(&S.drained, 0, a.status, 46);
+    if (rank == 0) wait_warp<(kSplits > 1)>(&S.drained, 0, a.status, 46);
   } else if (warp >= kRowWarp) {
     resolve_rows<kSplits>(S, rows, rank, warp - kRowWarp);
     cluster_wait();
@@ -836,11 +849,11 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_c
       if (r.nsel == 0 && r.klen > 0 && threadIdx.x == 0) set_status(a.status, DSA_ERR_OUT_OF_RANGE, t_out);
       sm.m = -INFINITY;
       sm.sum = 0.f;
-      for (int j = (n0 ^ g) & 1; j < r.nblk; j += 2) sm.block(S, a, tmem_lane, n0 + j, j, r.nblk, g, c, rank, to_first);
+      for (int j = (n0 ^ g) & 1; j < r.nblk; j += 2) sm.block<kSplits>(S, a, tmem_lane, n0 + j, j, r.nblk, g, c, rank, to_first);
       if (kSplits > 1) cluster_arrive();
       // the last block's group waits for its product (to the other group's threads the
       // barrier may still be two phases back); all meet at the barrier below
-      if (!empty && last == g) sm.dead = sm.dead || !wait_local(&S.pv_done[last], ((n0 + r.nblk - 1) >> 1) & 1, a.status, 52);
+      if (!empty && last == g) sm.dead = sm.dead || !wait_local<(kSplits > 1)>(&S.pv_done[last], ((n0 + r.nblk - 1) >> 1) & 1, a.status, 52);
       // the row's output: the head's maximum, its sum over four threads, then this
       // thread's half of the lane's columns
       const bool bad = named_bar_or(1, kSmThreads, sm.dead);
@@ -952,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_c
         const int col = kMine * grp;                // within the pair's columns
         float own[kMine];
         load_o(o_lane + sp * kCols + col, none, own);
-        const bool got = wait_local(&S.merged, 0, a.status, 57);
+        const bool got = wait_local<(kSplits > 1)>(&S.merged, 0, a.status, 57);
         // out = sum_s w_s O_s / sum_s w_s l_s,  w_s = 2^(m_s - max m), splits in order
         float w[kSplits];
         float2 v[kSplits];

@@ -263,8 +263,13 @@ dsa_status dsa_set_trace_buffer(void* dev_buf, size_t bytes);
  *       releases its accumulators, so its MMA issuer's wait for a free
  *       accumulator runs out (and then the epilogue's and the producer's
  *       waits for tiles that are never computed).
+ *   DSA_FAULT_MLA_INT4_VALUES  the attention over packed rows never announces
+ *       a decoded tile of values, so the wait of its second product's issuer
+ *       runs out (and then the waits for that product).  The rows that are
+ *       not finished for it end as NaN.
  * Returns DSA_ERR_INVALID_ARG for unknown fault bits.  (0, 0) switches it off. */
 #define DSA_FAULT_INDEXER_ACC_RELEASE 0x1u
+#define DSA_FAULT_MLA_INT4_VALUES 0x2u
 dsa_status dsa_set_fault_injection(uint32_t spin_limit, uint32_t faults);
 
 /* Stage 1: indexer scores.

@@ -25,6 +25,7 @@ DSA_KERNEL_OUT_PROJ, DSA_KERNEL_OUT_PROJ_REDUCE = 0x80, 0x100
 DSA_KERNEL_WARMUP = 0x200
 DSA_KERNEL_MLA_INT4_TC, DSA_KERNEL_CACHE_READ, DSA_KERNEL_BATCH_PLAN = 0x400, 0x800, 0x1000
 DSA_FAULT_INDEXER_ACC_RELEASE = 0x1
+DSA_FAULT_MLA_INT4_VALUES = 0x2
 
 
 class dsa_dims(ctypes.Structure):

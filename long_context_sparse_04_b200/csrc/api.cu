@@ -24,7 +24,7 @@ static void stage_event(int i, cudaStream_t s) {
 }
 
 long long* trace_buffer() { return g_trace; }
-uint32_t fault_spin_limit() { return g_fault_spin ? g_fault_spin : kSpinLimit; }
+uint32_t fault_spin_limit(uint32_t built_in) { return g_fault_spin ? g_fault_spin : built_in; }
 uint32_t fault_inject() { return g_fault_inject; }
 
 dsa_status set_smem_limit_once(const void* fn, size_t bytes, std::atomic<bool> (&done)[kMaxDevices]) {
@@ -528,7 +528,7 @@ dsa_status dsa_set_trace_buffer(void* dev_buf, size_t bytes) {
 }
 
 dsa_status dsa_set_fault_injection(uint32_t spin_limit, uint32_t faults) {
-  if ((faults & ~(uint32_t)DSA_FAULT_INDEXER_ACC_RELEASE) != 0) {
+  if ((faults & ~(uint32_t)(DSA_FAULT_INDEXER_ACC_RELEASE | DSA_FAULT_MLA_INT4_VALUES)) != 0) {
     set_error("unknown fault bits 0x%x", faults);
     return DSA_ERR_INVALID_ARG;
   }

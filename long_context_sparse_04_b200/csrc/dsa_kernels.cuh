@@ -67,6 +67,9 @@ struct MlaArgs {
   int splits;
   int merge_in_cluster;       // 2 splits in one 4-CTA cluster, merged through shared memory
   long long* trace;           // profiling stamps or null
+  // over packed rows
+  uint32_t spin_limit;        // polls of every bounded wait
+  uint32_t inject;            // DSA_FAULT_* bits (tests only)
 };
 
 struct AppendArgs {
@@ -123,9 +126,9 @@ struct PlanArgs {
 long long* trace_buffer();
 constexpr int kTraceMla = 0, kTraceTopk = 512, kTraceIdx = 640, kTraceLen = 896;
 // Test-only fault injection of the calling host thread (dsa_set_fault_injection):
-// the spin limit of the kernels' bounded waits (kSpinLimit unless set) and the
+// the spin limit of the kernels' bounded waits (`built_in` unless set) and the
 // DSA_FAULT_* bits to inject.
-uint32_t fault_spin_limit();
+uint32_t fault_spin_limit(uint32_t built_in);
 uint32_t fault_inject();
 static constexpr int kTraceEvents = 8, kTraceBlocks = 32;
 

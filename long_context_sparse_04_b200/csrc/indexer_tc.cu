@@ -579,7 +579,7 @@ dsa_status launch_nq(const IndexerArgs& a, cudaStream_t stream) {
     t.status = a.status;
     t.late_trigger = a.late_trigger;
     t.trace = trace_buffer() ? trace_buffer() + kTraceIdx : nullptr;
-    t.spin_limit = fault_spin_limit();
+    t.spin_limit = fault_spin_limit(kSpinLimit);
     t.inject = fault_inject();
     CUtensorMap tq;
     if (!make_tmap_rows128(&tq, static_cast<const uint8_t*>(a.q_idx) + (int64_t)r0 * kHI * kDI,

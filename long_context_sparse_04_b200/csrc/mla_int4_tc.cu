@@ -82,7 +82,9 @@ constexpr uint32_t kColS = 0, kColO = 64, kTmemCols = 512;
 // read by the softmax before its weights are stored, and resolving block n + 10 waits for
 // those (rows n + 6 loaded, keys n + 4 stored, S of block n + 2 done, weights n stored).
 constexpr int kRowRing = 4, kValidRing = 16;
-// polls of a bounded wait (20 ms at least; real waits take microseconds)
+// polls of a bounded wait (a poll that finds nothing takes up to 4 us: 4 s in all; real
+// waits take microseconds), unless a test sets fewer: read from the arguments, which costs
+// under 1 % of any case
 constexpr uint32_t kWaitPolls = 1u << 20;
 
 struct Smem {                                   // 1024-byte aligned
@@ -229,7 +231,7 @@ __device__ __forceinline__ void mma_commit_own(uint64_t* bar) {
 // against 30.3 us); in the persistent kernel, whose warps wait more, it was slower (16
 // heads: 27.5 against 26.6 us).
 template <bool kShort>
-__device__ __forceinline__ bool wait_local(uint64_t* bar, uint32_t parity, DeviceStatus* st, int site) {
+__device__ __forceinline__ bool wait_local(uint64_t* bar, uint32_t parity, const MlaArgs& a, int site) {
   uint32_t ok;
   if (kShort) {
     asm volatile(
@@ -249,14 +251,14 @@ __device__ __forceinline__ bool wait_local(uint64_t* bar, uint32_t parity, Devic
       "@q bra WAIT_%=;\n"
       "DONE_%=:\n\t"
       "selp.b32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "n"(kWaitPolls) : "memory");
-  if (!ok) set_status(st, DSA_ERR_TIMEOUT, site);
+      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "r"(a.spin_limit) : "memory");
+  if (!ok) set_status(a.status, DSA_ERR_TIMEOUT, site);
   return ok != 0;
 }
 // The same, agreed on by the warp (its lanes go on or leave together).
 template <bool kShort>
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, DeviceStatus* st, int site) {
-  return __all_sync(0xffffffffu, wait_local<kShort>(bar, parity, st, site));
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const MlaArgs& a, int site) {
+  return __all_sync(0xffffffffu, wait_local<kShort>(bar, parity, a, site));
 }
 // One arrival per warp on a barrier of the pair's first CTA.  What it announces
 // lies in the arriving CTA's own shared or tensor memory and is read by the tensor
@@ -286,18 +288,17 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
 template <int kSplits>
 __device__ __forceinline__ void issue_logits(Smem& S, RowStream<kSplits> rows, uint32_t tmem, uint16_t mask) {
   const MlaArgs& a = rows.a;
-  DeviceStatus* status = a.status;
   constexpr uint32_t idesc = idesc_bf16(kBlk, false);
   const uint64_t qd = sdesc_sw128(smem_u32(S.q), 16, 1024), kd0 = sdesc_sw128(smem_u32(S.k[0]), 16, 1024);
   Row r;
   bool ok = true;
   uint32_t busy = 0;                              // rows with keys so far
   for (int n0 = 0; ok && rows.next_busy(r); n0 += r.nblk, ++busy) {
-    ok = wait_local<(kSplits > 1)>(&S.q_full, busy & 1, status, 41);
+    ok = wait_local<(kSplits > 1)>(&S.q_full, busy & 1, a, 41);
     for (int j = 0; ok && j < r.nblk; ++j) {
       const int n = n0 + j, b = n & 1;
       // the keys are there, and S of block n-2 has been read: its weights are there
-      ok = wait_local<(kSplits > 1)>(&S.p_full[b], ((n >> 1) & 1) ^ 1, status, 43) && wait_local<(kSplits > 1)>(&S.k_full[b], (n >> 1) & 1, status, 42);
+      ok = wait_local<(kSplits > 1)>(&S.p_full[b], ((n >> 1) & 1) ^ 1, a, 43) && wait_local<(kSplits > 1)>(&S.k_full[b], (n >> 1) & 1, a, 42);
       if (!ok) break;
       tc_fence_after();
       const uint64_t kd = kd0 + (uint64_t)(b * (sizeof(S.k[0]) >> 4));
@@ -317,7 +318,6 @@ __device__ __forceinline__ void issue_logits(Smem& S, RowStream<kSplits> rows, u
 template <int kSplits>
 __device__ __forceinline__ void issue_outputs(Smem& S, RowStream<kSplits> rows, uint32_t tmem, uint16_t mask) {
   const MlaArgs& a = rows.a;
-  DeviceStatus* status = a.status;
   constexpr uint32_t idesc = idesc_bf16(256, true);
   const uint64_t pd0 = sdesc_sw128(smem_u32(S.p), 16, 1024), vd0 = sdesc_sw128(smem_u32(S.v[0]), kBlk * 128, 1024);
   Row r;
@@ -326,9 +326,9 @@ __device__ __forceinline__ void issue_outputs(Smem& S, RowStream<kSplits> rows, 
   for (int n0 = 0; ok && rows.next_busy(r); n0 += r.nblk, ++busy) {
     for (int j = 0; ok && j < r.nblk; ++j) {
       const int n = n0 + j, b = n & 1;
-      ok = wait_local<(kSplits > 1)>(&S.v_full[b], (n >> 1) & 1, status, 44) && wait_local<(kSplits > 1)>(&S.p_full[b], (n >> 1) & 1, status, 45);
+      ok = wait_local<(kSplits > 1)>(&S.v_full[b], (n >> 1) & 1, a, 44) && wait_local<(kSplits > 1)>(&S.p_full[b], (n >> 1) & 1, a, 45);
       // the row before has been read out of the accumulator
-      if (j == 0 && busy > 0) ok = ok && wait_local<(kSplits > 1)>(&S.o_free, (busy - 1) & 1, status, 58);
+      if (j == 0 && busy > 0) ok = ok && wait_local<(kSplits > 1)>(&S.o_free, (busy - 1) & 1, a, 58);
       if (!ok) break;
       tc_fence_after();
       const uint64_t vd = vd0 + (uint64_t)(b * (sizeof(S.v[0]) >> 4)), pd = pd0 + (uint64_t)(b * (sizeof(S.p[0]) >> 4));
@@ -343,7 +343,7 @@ __device__ __forceinline__ void issue_outputs(Smem& S, RowStream<kSplits> rows, 
     }
   }
   // the last row's arrivals from the other CTA are in
-  if (kSplits == 1 && ok && busy > 0) wait_local<(kSplits > 1)>(&S.o_free, (busy - 1) & 1, status, 58);
+  if (kSplits == 1 && ok && busy > 0) wait_local<(kSplits > 1)>(&S.o_free, (busy - 1) & 1, a, 58);
   mma_commit_own(&S.drained);
 }
 
@@ -426,7 +426,7 @@ __device__ __forceinline__ void resolve_rows(Smem& S, RowStream<kSplits> rows, u
     }
     positions();
     const int slot = n % kRowRing;
-    if (!wait_warp<(kSplits > 1)>(&S.rows_free[slot], (n / kRowRing & 1) ^ 1, a.status, 53)) break;
+    if (!wait_warp<(kSplits > 1)>(&S.rows_free[slot], (n / kRowRing & 1) ^ 1, a, 53)) break;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       int64_t row = (int64_t)e[u] + off[u];
@@ -511,7 +511,7 @@ __device__ __forceinline__ void decode_blocks(Smem& S, RowStream<kSplits> rows, 
   int v_row = -1;
   const auto load_keys = [&](int n) {
     const int slot = n % kRowRing;
-    if (!wait_warp<(kSplits > 1)>(&S.rows_full[slot], n / kRowRing & 1, a.status, 54)) return false;
+    if (!wait_warp<(kSplits > 1)>(&S.rows_full[slot], n / kRowRing & 1, a, 54)) return false;
     const int k_row = S.rows[slot][own + k_key], r_row = S.rows[slot][own + (kt >> 3)];
     v_row = S.rows[slot][v_key];
     warp_arrive(&S.rows_free[slot]);
@@ -567,12 +567,12 @@ __device__ __forceinline__ void decode_blocks(Smem& S, RowStream<kSplits> rows, 
       if (q_pending) {
         // Q's tile is free once S of the row before's last block has read it.  (A barrier
         // of its own: this group may not have seen the S before on that block's.)
-        if (!(ok = wait_warp<(kSplits > 1)>(&S.q_idle, (busy - 1) & 1, a.status, 59))) break;
+        if (!(ok = wait_warp<(kSplits > 1)>(&S.q_idle, (busy - 1) & 1, a, 59))) break;
         load_q(rows.t);
       }
       if (mine) {
         // the keys' stage is free once S of block n-2 has read it
-        if (!(ok = wait_warp<(kSplits > 1)>(&S.s_full[g], free, a.status, 47))) break;
+        if (!(ok = wait_warp<(kSplits > 1)>(&S.s_full[g], free, a, 47))) break;
         if (stamp) tstamp(a.trace, rank, 5, n);
         ku.store(k_dst);
         *reinterpret_cast<uint4*>(r_dst) = rope;
@@ -585,22 +585,22 @@ __device__ __forceinline__ void decode_blocks(Smem& S, RowStream<kSplits> rows, 
       // parity tells two phases apart, not three, and such a row could end without this
       // group.
       const bool idle_wait = first_in_row && busy > 0;
-      if (idle_wait && !mine && !(ok = wait_warp<(kSplits > 1)>(&S.v_idle[g], (busy - 1) & 1, a.status, 60))) break;
+      if (idle_wait && !mine && !(ok = wait_warp<(kSplits > 1)>(&S.v_idle[g], (busy - 1) & 1, a, 60))) break;
       if (q_pending) {
         q_landed();
         q_pending = false;
       }
       const bool more = mine && comes(n + 2);
       if (more && !(ok = load_keys(n + 2))) break;
-      if (idle_wait && mine && !(ok = wait_warp<(kSplits > 1)>(&S.v_idle[g], (busy - 1) & 1, a.status, 60))) break;
+      if (idle_wait && mine && !(ok = wait_warp<(kSplits > 1)>(&S.v_idle[g], (busy - 1) & 1, a, 60))) break;
       first_in_row = false;
       if (mine) {
         // the values' stage is free once P V of block n-2 has read it
-        if (!(ok = wait_warp<(kSplits > 1)>(&S.pv_done[g], free, a.status, 48))) break;
+        if (!(ok = wait_warp<(kSplits > 1)>(&S.pv_done[g], free, a, 48))) break;
         if (stamp) tstamp(a.trace, rank, 7, n);
         vu.store(v_dst);
         fence_proxy_async_smem();
-        warp_arrive_first(&S.v_full[g], first);
+        if (!(a.inject & DSA_FAULT_MLA_INT4_VALUES)) warp_arrive_first(&S.v_full[g], first);
         if (stamp) tstamp(a.trace, rank, 1, n);
         if (more) load_values();
       }
@@ -668,8 +668,8 @@ struct Softmax {
     const uint32_t phase = (n >> 1) & 1;
     // the weights' tile is free once P V of block n-2 has read it (waited for here, where
     // the group waits for its logits anyway)
-    dead = dead || !wait_local<(kSplits > 1)>(&S.pv_done[g], phase ^ 1, a.status, 51);
-    dead = dead || !wait_local<(kSplits > 1)>(&S.s_full[g], phase, a.status, 49);
+    dead = dead || !wait_local<(kSplits > 1)>(&S.pv_done[g], phase ^ 1, a, 51);
+    dead = dead || !wait_local<(kSplits > 1)>(&S.s_full[g], phase, a, 49);
     tc_fence_after();
     if (l == 0 && a.trace != nullptr) tstamp(a.trace, rank, 4, n);
     float s[32];
@@ -706,7 +706,7 @@ struct Softmax {
       const float alpha = need ? (m_now == -INFINITY ? 0.f : exp2f(m_now - m_new)) : 1.f;
       if (j > 0) {
         // no product is in flight: block j-1's is done, block j's waits for P below
-        dead = dead || !wait_local<(kSplits > 1)>(&S.pv_done[g ^ 1], ((n - 1) >> 1) & 1, a.status, 50);
+        dead = dead || !wait_local<(kSplits > 1)>(&S.pv_done[g ^ 1], ((n - 1) >> 1) & 1, a, 50);
         tc_fence_after();
 #pragma unroll 1
         for (int cc = 0; cc < 16; ++cc) {
@@ -824,9 +824,14 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_c
       else issue_outputs<kSplits>(S, rows, tmem, (uint16_t)(3u << first));
     }
     __syncwarp();
-    cluster_arrive();
-    // every product issued is done before the pair's shared and tensor memory go
-    if (rank == 0) wait_warp<(kSplits > 1)>(&S.drained, 0, a.status, 46);
+    // Every product issued is done before the pair's shared and tensor memory go, even if
+    // all others have left because waits ran out: waited for (with the built-in limit)
+    // before the cluster's last barrier.  Without splits that is this one; with them the
+    // merge may begin, and the last one follows it.
+    if (kSplits > 1) cluster_arrive();
+    if (rank == 0) mbar_wait(&S.drained, 0, a.status, 46);
+    __syncwarp();
+    if (kSplits == 1) cluster_arrive();
   } else if (warp >= kRowWarp) {
     resolve_rows<kSplits>(S, rows, rank, warp - kRowWarp);
     cluster_wait();
@@ -853,15 +858,16 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_c
       if (kSplits > 1) cluster_arrive();
       // the last block's group waits for its product (to the other group's threads the
       // barrier may still be two phases back); all meet at the barrier below
-      if (!empty && last == g) sm.dead = sm.dead || !wait_local<(kSplits > 1)>(&S.pv_done[last], ((n0 + r.nblk - 1) >> 1) & 1, a.status, 52);
+      if (!empty && last == g) sm.dead = sm.dead || !wait_local<(kSplits > 1)>(&S.pv_done[last], ((n0 + r.nblk - 1) >> 1) & 1, a, 52);
       // the row's output: the head's maximum, its sum over four threads, then this
       // thread's half of the lane's columns
       const bool bad = named_bar_or(1, kSmThreads, sm.dead);
       settled = settled && !bad;
       tc_fence_after();
       const float M = empty ? -INFINITY : S.m_run[last][hl];
-      // (a maximum of -inf goes with a sum of 0, or NaN from a NaN logit, which stays)
-      S.red[g][l] = bad ? __int_as_float(0x7FC00000) : sm.m == -INFINITY ? sm.sum : sm.sum * exp2f(sm.m - M);
+      // (a maximum of -inf goes with a sum of 0, or NaN from a NaN logit, which stays; a row
+      // without a key depends on no wait)
+      S.red[g][l] = bad && !empty ? __int_as_float(0x7FC00000) : sm.m == -INFINITY ? sm.sum : sm.sum * exp2f(sm.m - M);
       if (kSplits > 1) break;
       named_bar_sync(1, kSmThreads);
       const float L = (S.red[0][hl] + S.red[1][hl]) + (S.red[0][hl + 64] + S.red[1][hl + 64]);
@@ -965,7 +971,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_int4_tc_kernel(const __grid_c
         const int col = kMine * grp;                // within the pair's columns
         float own[kMine];
         load_o(o_lane + sp * kCols + col, none, own);
-        const bool got = wait_local<(kSplits > 1)>(&S.merged, 0, a.status, 57);
+        const bool got = wait_local<(kSplits > 1)>(&S.merged, 0, a, 57);
         // out = sum_s w_s O_s / sum_s w_s l_s,  w_s = 2^(m_s - max m), splits in order
         float w[kSplits];
         float2 v[kSplits];
@@ -1118,7 +1124,10 @@ dsa_status launch_mla_int4_tc(const MlaArgs& a, cudaStream_t stream) {
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, out_map);
+  MlaArgs la = a;
+  la.spin_limit = fault_spin_limit(kWaitPolls);
+  la.inject = fault_inject();
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, la, out_map);
   if (e != cudaSuccess) {
     set_error("mla_int4_tc launch: %s", cudaGetErrorString(e));
     return DSA_ERR_CUDA;

@@ -467,14 +467,18 @@ typedef struct {
  * the row_seq of the last planned row (0 if none), so that dsa_rows of max_tokens
  * rows and dsa_cache_append_slots may run on the padded batch: a captured graph
  * needs no host decision.  With a contiguous cache (block_table NULL) there are no
- * pages: slot = seq_start[b] + tok_pos, and a request beyond num_tokens is refused.
+ * pages: slot = seq_start[b] + tok_pos.  The rows of a request end where the next
+ * larger seq_start of any request (active or not, in any order) begins, or at
+ * num_tokens; a request beyond them is refused, and so is one that asks for tokens
+ * where another that holds or asks for tokens has the same seq_start (NULL: all 0).
  * Free-list entries at and above free_count_out are unspecified where pages were
  * handed back, and as they were elsewhere.
  * Device errors (the lowest such request is the detail): DSA_ERR_INVALID_ARG for a
  * negative length or count, a seq_len beyond the block table, a release with
  * n_new != 0 (such a request is left as it is), or a free count outside
  * [0, free_capacity] (taken as 0); DSA_ERR_OUT_OF_RANGE for a
- * request longer than its row of the block table (refused), and for a page id
+ * request longer than its row of the block table or than its rows of a contiguous
+ * cache (refused), and for a page id
  * outside the cache, whose block-table entry and slots become -1.
  * B <= 16384 and B * max_pages_per_seq < 2^31.  Deterministic; one kernel.
  * ws: dsa_workspace_size(NULL, NULL, DSA_OP_BATCH_PLAN) bytes (the status block),

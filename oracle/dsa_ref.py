@@ -607,8 +607,12 @@ def batch_plan(seq_len, n_new, release, free_list, block_table, page_size, num_p
         if table is not None:
             too_long = L + n > W * P
         else:
-            start = 0 if seq_start is None else int(seq_start[b])
-            too_long = start < 0 or start + L + n > num_tokens
+            # the rows end where another sequence's begin
+            starts = [0] * B if seq_start is None else [int(x) for x in seq_start]
+            start = starts[b]
+            shared = any(starts[c] == start and (old[c] > 0 or int(n_new[c]) > 0) for c in range(B) if c != b)
+            end = min([num_tokens] + [x for x in starts if x > start])
+            too_long = start < 0 or shared or start + L + n > end
         if too_long or L + n > 2 ** 31 - 1:
             errors[b] = "range"
         else:

@@ -9,16 +9,20 @@
 // pages and rows asked for (the admission) in one scan, pages and rows granted in
 // another.  Every CTA computes them for itself, keeps the three that the rest needs in
 // shared memory, and writes its share of the rows, table entries and pages; a binary
-// search in shared memory gives a row's request.  One CTA plans a decoding batch; a
-// chunked prefill of 131,072 rows takes 128 (redoing the sums costs them nothing: one
-// CTA after another would wait for them all the same, and a cluster, which could share
-// them, is 8 CTAs).  What bounds it is latency: the launch, two loads in a chain, the
-// scans' barriers, the searches.
+// search in shared memory gives a row's request.  CTAs are launched by what the host
+// knows: for the rows (a chunked prefill of 131,072 takes 128), and for the pages that a
+// step may hand back (redoing the sums costs them nothing: one CTA after another would
+// wait for them all the same, and a cluster, which could share them, is 8 CTAs).  200
+// requests of up to 128K tokens in pages of 16 that hand back 239,770 take 24 us with 16
+// CTAs and runs of eight pages a thread, 150 with one CTA, 519 without the runs as well;
+// where nothing is handed back the further CTAs cost 0.2 us.  What bounds it is latency:
+// the launch, two loads in a chain, the scans' barriers, the searches.
 // Lengths and the free count, which may be updated in place, are written by the CTA
 // that finishes last, when every CTA has read them; free-list entries read (below the
 // old count) and written (at or above it) never meet, nor do table entries read (pages
 // held) and written.
 #include <climits>
+#include <type_traits>
 
 #include "dsa_kernels.cuh"
 
@@ -29,6 +33,7 @@ namespace {
 // requests: 6.5 us a plan with 256 threads, 7.8 with 1,024 and three scans; 4,096
 // requests and 131,072 rows: 18.0).
 constexpr int kFew = 256, kMany = 1024;
+constexpr int kFewCtas = 16;           // at most, for the pages that may be handed back
 constexpr int kMaxSeqs = 16384;        // three int32 prefix arrays in shared memory
 
 // One request as the rule sees it.
@@ -341,7 +346,28 @@ __global__ void __launch_bounds__(kThreads, 1) batch_plan_kernel(const __grid_co
     a.block_table[(int64_t)b * W + held + (k - pg_start[b])] = taken_page(k);
   }
   const int64_t left = min(have - taken, (int64_t)a.p.free_capacity);
-  for (int64_t i = F + gid; i < left; i += step) a.p.free_pages[i] = handed_back((int32_t)(i - F));
+  // Pages handed back, in runs of kRun * 32 a warp: one search where a run is one request's,
+  // and all its loads in flight before its first store.
+  const int32_t back = (int32_t)max(left - F, (int64_t)0);
+  const auto hand_back = [&](auto run) {
+    constexpr int kRun = decltype(run)::value;
+    for (int64_t i64 = (int64_t)(gid >> 5) * (32 * kRun); i64 < back; i64 += (int64_t)step * kRun) {
+      const int32_t i0 = (int32_t)i64, b0 = owner(give_start, B, i0), end = give_start[b0 + 1];
+      int32_t page[kRun];
+#pragma unroll
+      for (int u = 0; u < kRun; ++u) {
+        const int32_t i = i0 + 32 * u + (tid & 31), b = i < end ? b0 : owner(give_start, B, min(i, back - 1));
+        if (i < back) page[u] = a.block_table[(int64_t)b * W + (i - give_start[b])];
+      }
+#pragma unroll
+      for (int u = 0; u < kRun; ++u) {
+        const int32_t i = i0 + 32 * u + (tid & 31);
+        if (i < back) a.p.free_pages[F + i] = page[u];
+      }
+    }
+  };
+  if (back <= step) hand_back(std::integral_constant<int, 1>());
+  else hand_back(std::integral_constant<int, 8>());
   for (int b = gid; b <= B; b += step) a.p.tok_start[b] = tok_start[b];
 
   // the CTA that is done last has the rest: every CTA has read the lengths and the free
@@ -378,6 +404,12 @@ __global__ void __launch_bounds__(kThreads, 1) batch_plan_kernel(const __grid_co
 
 int batch_plan_max_seqs() { return kMaxSeqs; }
 
+// CTAs for n items, `each` a CTA: one at least, `most` at most.
+static int ctas_for(int64_t n, int each, int most) {
+  const int64_t want = (n + each - 1) / each;
+  return want < 1 ? 1 : want < most ? (int)want : most;
+}
+
 template <bool kPaged>
 static dsa_status launch(const PlanArgs& a, cudaStream_t stream) {
   const size_t smem_max = (size_t)3 * (kMaxSeqs + 1) * sizeof(int32_t);
@@ -385,13 +417,15 @@ static dsa_status launch(const PlanArgs& a, cudaStream_t stream) {
   if (dsa_status st = set_smem_limit_once(reinterpret_cast<const void*>(batch_plan_kernel<kMany, kPaged>), smem_max, attr))
     return st;
   const size_t smem = (size_t)3 * (a.num_seqs + 1) * sizeof(int32_t);
+  // The pages that a step may hand back are as many as the tables or the cache hold: known
+  // here only as that bound, so CTAs are launched for them that mostly find nothing to do.
+  const int64_t table = (int64_t)a.num_seqs * a.max_pages_per_seq;
+  const int64_t back = !kPaged || a.p.release == nullptr ? 0 : table < a.num_pages ? table : a.num_pages;
   if (a.num_seqs <= 2 * kFew && a.p.max_tokens <= 8 * kFew) {
-    batch_plan_kernel<kFew, kPaged><<<1, kFew, smem, stream>>>(a);
+    batch_plan_kernel<kFew, kPaged><<<ctas_for(back, 16 * kFew, kFewCtas), kFew, smem, stream>>>(a);
   } else {
-    // a CTA for every kMany rows, at most one per SM
-    const int64_t want = ((int64_t)a.p.max_tokens + kMany - 1) / kMany;
-    const int most = device_sm_count(), ctas = want < 1 ? 1 : want < most ? (int)want : most;
-    batch_plan_kernel<kMany, kPaged><<<ctas, kMany, smem, stream>>>(a);
+    const int most = device_sm_count(), rows = ctas_for(a.p.max_tokens, kMany, most), pages = ctas_for(back, 8 * kMany, most);
+    batch_plan_kernel<kMany, kPaged><<<rows > pages ? rows : pages, kMany, smem, stream>>>(a);
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {

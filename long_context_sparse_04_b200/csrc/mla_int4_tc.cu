@@ -61,6 +61,7 @@
 #include "dsa_int4.cuh"
 #include "dsa_kernels.cuh"
 #include "mla_common.cuh"
+#include "mla_int4_shape.h"
 
 namespace dsa {
 namespace {
@@ -1052,9 +1053,9 @@ bool make_out_map(CUtensorMap* m, const MlaArgs& a) {
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaLaunchConfig_t launch_config(cudaLaunchAttribute (&at)[2], int splits, int rows) {
+cudaLaunchConfig_t launch_config(cudaLaunchAttribute (&at)[2], int splits, int clusters) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * splits * 2));
+  cfg.gridDim = dim3((unsigned)(clusters * splits * 2));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = sizeof(Smem);
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -1066,23 +1067,22 @@ cudaLaunchConfig_t launch_config(cudaLaunchAttribute (&at)[2], int splits, int r
   return cfg;
 }
 
-// Clusters of `splits` pairs that can be resident at once on this device (0 if the
-// query fails), looked up once per device.
+// Clusters of `splits` pairs that can be resident at once on this device, negative if the
+// query fails.  Kept per device; a context with a part of the SMs then gets the number of
+// the context that asked first, which is a matter of speed only.
 int resident_clusters(Kernel kernel, int splits) {
-  static std::atomic<int> cached[kMaxPairs + 1][kMaxDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
-  const int have = cached[splits][dev].load();
-  if (have > 0) return have - 1;
-  cudaLaunchAttribute at[2];
-  cudaLaunchConfig_t cfg = launch_config(at, splits, 1);
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+  static OnceAsked kept[kMaxPairs + 1][kMaxDevices];
+  const auto ask = [&] {
+    cudaLaunchAttribute at[2];
+    cudaLaunchConfig_t cfg = launch_config(at, splits, 1);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess) return n;
     (void)cudaGetLastError();
-    n = 0;
-  }
-  cached[splits][dev].store(n + 1);
-  return n;
+    return -1;
+  };
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  return dev < kMaxDevices ? kept[splits][dev].get(ask) : ask();
 }
 
 }  // namespace
@@ -1104,22 +1104,12 @@ dsa_status launch_mla_int4_tc(const MlaArgs& a, cudaStream_t stream) {
       (st = set_smem_limit_once(reinterpret_cast<const void*>(kernel_of<2>), sizeof(Smem), attr2)) ||
       (st = set_smem_limit_once(reinterpret_cast<const void*>(kernel_of<4>), sizeof(Smem), attr4)))
     return st;
-  // key splits: the most whose clusters are all resident at once (a second wave costs
-  // more than a split saves), where the selection has a block of keys for each
-  int splits = 1;
-  Kernel kernel = kernel_of<1>;
-  if (a.topk > 2 * kBlk && a.num_rows <= resident_clusters(kernel_of<4>, 4)) {
-    splits = 4;
-    kernel = kernel_of<4>;
-  } else if (a.topk > kBlk && a.num_rows <= resident_clusters(kernel_of<2>, 2)) {
-    splits = 2;
-    kernel = kernel_of<2>;
-  }
+  const auto kernel_for = [](int splits) { return splits == 4 ? kernel_of<4> : splits == 2 ? kernel_of<2> : kernel_of<1>; };
+  const Int4Shape shape = int4_shape(a.num_rows, a.topk, kBlk, device_sm_count(),
+                                     [&](int splits) { return resident_clusters(kernel_for(splits), splits); });
+  Kernel kernel = kernel_for(shape.splits);
   cudaLaunchAttribute at[2];
-  // without splits one resident wave of pairs shares the rows
-  int clusters = a.num_rows;
-  if (splits == 1) clusters = min(clusters, max(resident_clusters(kernel, 1), 1));
-  cudaLaunchConfig_t cfg = launch_config(at, splits, clusters);
+  cudaLaunchConfig_t cfg = launch_config(at, shape.splits, shape.clusters);
   cfg.stream = stream;
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;

@@ -79,8 +79,11 @@ typedef enum {
  *                         half is dim 2i, nibble i of the high half dim 2i + 1
  *   then 2*d_r bytes      the RoPE key, bf16, as given
  *   then d_c/16 bytes     one scale per 16 consecutive latent dims, an unsigned
- *                         8-bit float of 5 exponent and 3 mantissa bits: the
- *                         fp16 number whose bit pattern is the byte << 7
+ *                         8-bit float with 5 exponent bits e (bias 15) and 3
+ *                         mantissa bits m, byte = 8 e + m: (8 + m) * 2^(e - 18),
+ *                         and m * 2^-17 for e = 0.  There is no infinity or NaN:
+ *                         the bytes 0xF8 to 0xFF are 65536 to 122880.  (Up to
+ *                         0xF7 it is the fp16 number of bit pattern byte << 7.)
  *   then zeros up to a multiple of 16 bytes
  * (416 bytes for d_c = 512, d_r = 64; dsa_latent_row_bytes).  The value of a
  * dim is code * scale: at most 4 + 4 significant bits, so it is exact in bf16.

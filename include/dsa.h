@@ -306,7 +306,11 @@ dsa_status dsa_topk(const dsa_dims* dims, const dsa_rows* rows, const float* sco
  *       first klen[t] entries, as dsa_topk leaves them)
  *   out [T, H, d_c] bf16 | f32 (same dtype as q)
  *   lse [T, H] fp32 natural-log sum of exp(z) (may be NULL); -inf and out = 0
- *       for a row with no selected key. */
+ *       for a row with no selected key.
+ * A row_seq outside [0, num_seqs) of a paged cache or one with seq_start is a
+ * caller error: the CUDA-core kernels (every type) and those over packed rows read
+ * nothing for that row (out = 0, lse = -inf) and record DSA_ERR_OUT_OF_RANGE with
+ * the row as detail; the bf16 tensor-core kernel reads as given. */
 dsa_status dsa_sparse_mla_fwd(const dsa_dims* dims, const dsa_rows* rows, const dsa_cache* cache,
                               const void* q, const int32_t* idx, void* out, float* lse,
                               void* ws, size_t ws_bytes, dsa_stream_t stream);

@@ -465,6 +465,9 @@ typedef struct {
  *     n_new[b] = 0  or  n_new[0] + ... + n_new[b] <= max_tokens,
  * sums over all requests that could run, planned or not.  A request that is not
  * planned keeps its length, gets no rows and counts as refused; that is no error.
+ * So no request overtakes one that waits for pages or rows: one that waits holds up
+ * those behind it that ask for some, and one with n_new > max_tokens does so in every
+ * step (totals[2] shows it; hand over at most max_tokens tokens of a prompt at once).
  * Pages are popped from the top of the list in request and page order; their ids
  * are written into the request's row of cache->block_table (written here; the
  * descriptor is shared with the calls that read it), and seq_len_out = seq_len +
@@ -478,6 +481,8 @@ typedef struct {
  * larger seq_start of any request (active or not, in any order) begins, or at
  * num_tokens; a request beyond them is refused, and so is one that asks for tokens
  * where another that holds or asks for tokens has the same seq_start (NULL: all 0).
+ * Every page belongs to one request or to the free list, once: a page that stands in
+ * two rows of the table would be handed back twice.
  * Free-list entries at and above free_count_out are unspecified where pages were
  * handed back, and as they were elsewhere.
  * Device errors (the lowest such request is the detail): DSA_ERR_INVALID_ARG for a

@@ -128,23 +128,6 @@ __device__ __forceinline__ bool position_row(const AppendArgs& a, int seq, int p
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// Two fp32 in one 64-bit register pair: one instruction for both.
-__device__ __forceinline__ uint64_t pair_f32(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // The code words of a group whose scale's reciprocal is r.
 __device__ __forceinline__ void int4_codes(const uint32_t (&v)[8], float r, uint32_t (&w)[2]) {
   const uint64_t r2 = pair_f32(r, r), to_grid = pair_f32(6144.f, 6144.f), to_int = pair_f32(12576768.f, 12576768.f);

@@ -1,6 +1,5 @@
 // mla_common.cuh - what the tensor-core attention kernels (bf16 rows, packed
-// 4-bit rows) share: softmax constants, roundings, and the arrival tickets of the
-// key splits.
+// 4-bit rows) share: softmax constants, roundings and profiling stamps.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -9,7 +8,6 @@
 
 namespace dsa {
 
-constexpr int kMaxSplits = 8;                 // key splits of a decode row, a power of 2
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;
@@ -31,31 +29,10 @@ __device__ __forceinline__ uint4 pack8(const float* f, float inv) {
   return make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
                     pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
 }
-// Arrival ticket of one of a row's key splits: the slot holds (launch id << 32 |
-// arrivals); a slot tagged with another launch (an earlier one, or never
-// written) counts as empty, and the last arrival resets the count, so the
-// slots need no clearing between launches.
-// Returns the arrivals of this launch, this one included (0 if the CAS loop,
-// which only ever competes with the row's other splits, were to run away).
-__device__ __forceinline__ uint32_t take_ticket(unsigned long long* slot, uint32_t id, DeviceStatus* st) {
-  unsigned long long cur = *reinterpret_cast<volatile unsigned long long*>(slot);
-  for (int it = 0; it < 1 << 16; ++it) {
-    const unsigned long long nv =
-        (uint32_t)(cur >> 32) == id ? cur + 1ull : ((unsigned long long)id << 32) | 1ull;
-    const unsigned long long got = atomicCAS(slot, cur, nv);
-    if (got == cur) return (uint32_t)nv;
-    cur = got;
-  }
-  set_status(st, DSA_ERR_TIMEOUT, 29);
-  return 0u;
-}
-
 // Profiling stamp: event `ev` of block j in the first cluster's first pair.
 __device__ __forceinline__ void tstamp(long long* tr, uint32_t rank, int ev, int j) {
   if (tr != nullptr && blockIdx.x < 2 && j < kTraceBlocks)
     tr[((int)rank * kTraceEvents + ev) * kTraceBlocks + j] = clock64();
 }
-
-uint32_t next_launch_id();
 
 }  // namespace dsa

@@ -51,6 +51,7 @@ constexpr int kH = 128, kDC = 512, kDR = 64, kD = kDC + kDR;
 constexpr int kBlk = 64;
 constexpr int kNS = 3;
 constexpr int kMaxKeys = 2048;
+constexpr int kMaxSplits = 8;                 // key splits of a decode row, a power of 2
 constexpr int kGatherWarp0 = 1, kGatherWarps = 15;
 constexpr int kGatherThreads = 32 * kGatherWarps;       // 480
 constexpr int kExWarp0 = 16;                            // warps 16-19
@@ -159,6 +160,25 @@ __device__ __forceinline__ void stage_bf16(uint8_t* stg, int h, int c0, const fl
   for (int q = 0; q < 4; ++q)
     *reinterpret_cast<uint4*>(stg + h * 512 + (((c0 + q) ^ (h & 31)) << 4)) = pack8(&o[8 * q], inv);
 }
+// Arrival ticket of one of a row's key splits: the slot holds (launch id << 32 |
+// arrivals); a slot tagged with another launch (an earlier one, or never
+// written) counts as empty, and the last arrival resets the count, so the
+// slots need no clearing between launches.
+// Returns the arrivals of this launch, this one included (0 if the CAS loop,
+// which only ever competes with the row's other splits, were to run away).
+__device__ __forceinline__ uint32_t take_ticket(unsigned long long* slot, uint32_t id, DeviceStatus* st) {
+  unsigned long long cur = *reinterpret_cast<volatile unsigned long long*>(slot);
+  for (int it = 0; it < 1 << 16; ++it) {
+    const unsigned long long nv =
+        (uint32_t)(cur >> 32) == id ? cur + 1ull : ((unsigned long long)id << 32) | 1ull;
+    const unsigned long long got = atomicCAS(slot, cur, nv);
+    if (got == cur) return (uint32_t)nv;
+    cur = got;
+  }
+  set_status(st, DSA_ERR_TIMEOUT, 29);
+  return 0u;
+}
+
 __device__ __forceinline__ void setmaxnreg_inc_high() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
 }
@@ -746,14 +766,6 @@ int mla_tc_splits(int num_rows) {
   return s;
 }
 
-// A launch id for the split arrival tickets: distinct for consecutive launches, never 0.
-uint32_t next_launch_id() {
-  static std::atomic<uint32_t> launch_seq{0};
-  uint32_t id;
-  do id = launch_seq.fetch_add(1u) + 1u; while (id == 0u);
-  return id;
-}
-
 // Split-K scratch: partial O (fp32) and (max, sum) per (row, split, head), then
 // one 8-byte arrival ticket per (row, CTA rank).
 size_t mla_ws_bytes(int num_rows, int n_heads, int d_c, int splits) {
@@ -845,7 +857,9 @@ dsa_status launch_mla_tc(const MlaArgs& a, cudaStream_t stream) {
   attr2[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr2;
   cfg.numAttrs = 2;
-  la.launch_id = next_launch_id();
+  // a launch id for the split arrival tickets: distinct for consecutive launches, never 0
+  static std::atomic<uint32_t> launch_seq{0};
+  do la.launch_id = launch_seq.fetch_add(1u) + 1u; while (la.launch_id == 0u);
   cudaError_t e = cudaLaunchKernelEx(&cfg, mla_tc_kernel, la, keys_per_split);
   if (e != cudaSuccess) {
     set_error("mla_tc launch: %s", cudaGetErrorString(e));

@@ -260,10 +260,14 @@ class DevicePlanner:
 
 class PagedCache:
     """The caches of one layer behind a DevicePlanner: FP8 indexer keys, and the
-    latents in bf16 or in packed 4-bit rows."""
+    latents in bf16 or in packed 4-bit rows.
+
+    workspace_of: the cache of another layer of the same planner, whose workspace (the
+    scores of a step above all: rows x context x 4 bytes) this one then uses.  The
+    layers' calls must run one after the other, and share one status word."""
 
     def __init__(self, planner: DevicePlanner, n_heads: int = 128, topk: int = 2048, int4: bool = True,
-                 sm_scale: float | None = None, q_group: int = 1):
+                 sm_scale: float | None = None, q_group: int = 1, workspace_of: "PagedCache | None" = None):
         torch = self.torch = planner.torch
         self.planner = planner
         d_c, d_r, d_idx = 512, 64, 128
@@ -283,8 +287,15 @@ class PagedCache:
         self.idx = torch.full((p.max_tokens, topk), -1, dtype=torch.int32, device=dev)
         with p.on_device():
             nb = N.dsa_workspace_size(self.dims, self.rows, N.DSA_OP_DECODE_STEP)
-            self._ws = torch.empty(nb, dtype=torch.uint8, device=dev)
-            N.dsa_workspace_init(_vp(self._ws), nb, p.stream)
+            if workspace_of is None:
+                self._ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+                N.dsa_workspace_init(_vp(self._ws), nb, p.stream)
+            elif workspace_of.planner is not planner:
+                raise ValueError("workspace_of: a layer of another planner")
+            elif workspace_of._ws.numel() < nb:
+                raise ValueError(f"workspace_of: {workspace_of._ws.numel()} bytes, {nb} needed")
+            else:
+                self._ws = workspace_of._ws
 
     def _args(self):
         return _vp(self._ws), self._ws.numel(), self.planner.stream

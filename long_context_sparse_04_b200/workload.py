@@ -36,15 +36,21 @@ def pack_latents(dims, latent):
     """Packed 4-bit rows (uint8 [n, row bytes]) of bf16 latent rows on a device."""
     import torch
     n = latent.shape[0]
+    if not latent.is_cuda:
+        raise ValueError("latent: a tensor on a CUDA device expected")
+    new = _tensor(latent, "latent", (n, dims.d_c + dims.d_r), (torch.bfloat16,), latent.device)
     packed = torch.empty((n, N.dsa_latent_row_bytes(dims)), dtype=torch.uint8, device=latent.device)
+    if n == 0:
+        return packed
     slot = torch.arange(n, dtype=torch.int64, device=latent.device)
     ws = torch.zeros(N.dsa_workspace_size(dims, None, N.DSA_OP_CACHE_APPEND), dtype=torch.uint8, device=latent.device)
     cache = N.dsa_cache(latent=_vp(packed), num_seqs=1, num_tokens=n)
     stream = ctypes.c_void_p(torch.cuda.current_stream(latent.device).cuda_stream)
     with torch.cuda.device(latent.device):
-        N.dsa_cache_append_slots(dims, cache, n, _vp(slot), None, _vp(latent), _vp(ws), ws.numel(), stream)
+        N.dsa_cache_append_slots(dims, cache, n, _vp(slot), None, new, _vp(ws), ws.numel(), stream)
         st = N.dsa_read_device_status(_vp(ws), stream)
-    assert st == (0, -1), f"latent row {st[1]} has an infinity or NaN"
+    if st != (0, -1):
+        raise ValueError(f"latent row {st[1]} has an infinity or NaN")
     return packed
 
 
@@ -206,6 +212,15 @@ class DeviceWorkload:
         return self.k_idx.cpu().numpy(), ks, lat
 
 
+def _tensor(x, name: str, shape, dtypes, device):
+    """Device pointer of an argument that a kernel will take at its word."""
+    if tuple(x.shape) != tuple(shape) or x.dtype not in dtypes or x.device != device or not x.is_contiguous():
+        want = " or ".join(str(d) for d in dtypes)
+        raise ValueError(f"{name}: contiguous {want} of shape {tuple(shape)} on {device} expected, got {x.dtype} of shape "
+                         f"{tuple(x.shape)} on {x.device}{'' if x.is_contiguous() else ', not contiguous'}")
+    return _vp(x)
+
+
 class DevicePlanner:
     """The paging state of a batch of request slots, planned on the GPU: lengths,
     block table and free list live in device memory and each plan() (one
@@ -300,22 +315,39 @@ class PagedCache:
     def _args(self):
         return _vp(self._ws), self._ws.numel(), self.planner.stream
 
+    def _arg(self, x, name, shape, *dtypes):
+        return _tensor(x, name, shape, dtypes, self.planner.seq_len.device)
+
     def append(self, k_new, latent_new):
-        """The planned step's tokens (rows of max_tokens) into the caches."""
+        """The planned step's tokens into the caches: max_tokens rows, in the plan's order,
+        whatever lies behind the last."""
+        torch, M, d = self.torch, self.planner.max_tokens, self.dims
+        k = self._arg(k_new, "k_new", (M, d.d_idx), torch.float32)
+        lat = self._arg(latent_new, "latent_new", (M, d.d_c + d.d_r), torch.bfloat16)
         with self.planner.on_device():
-            N.dsa_cache_append_slots(self.dims, self.cache, self.planner.max_tokens, _vp(self.planner.slot), _vp(k_new),
-                                     _vp(latent_new), *self._args())
+            N.dsa_cache_append_slots(d, self.cache, M, _vp(self.planner.slot), k, lat, *self._args())
 
     def read(self, slot, k_out=None, latent_out=None):
         """Cached tokens by physical row, as the values they stand for."""
+        torch, n, d = self.torch, int(slot.shape[0]), self.dims
+        at = self._arg(slot, "slot", (n,), torch.int64)
+        k = None if k_out is None else self._arg(k_out, "k_out", (n, d.d_idx), torch.float32)
+        lat = None if latent_out is None else self._arg(latent_out, "latent_out", (n, d.d_c + d.d_r), torch.bfloat16)
         with self.planner.on_device():
-            N.dsa_cache_read(self.dims, self.cache, int(slot.shape[0]), _vp(slot), _vp(k_out), _vp(latent_out), *self._args())
+            N.dsa_cache_read(d, self.cache, n, at, k, lat, *self._args())
 
     def decode_step(self, q_idx, q_scale, w, q, out, lse=None):
-        """The three stages over the planned rows; rows behind the last give 0 and -inf."""
+        """The three stages over the planned rows (max_tokens rows in every tensor); rows
+        behind the last give 0 and -inf."""
+        torch, M, d = self.torch, self.planner.max_tokens, self.dims
+        args = (self._arg(q_idx, "q_idx", (M, d.n_idx_heads, d.d_idx), torch.uint8, torch.float8_e4m3fn),
+                self._arg(q_scale, "q_scale", (M, d.n_idx_heads), torch.float32),
+                self._arg(w, "w", (M, d.n_idx_heads), torch.float32),
+                self._arg(q, "q", (M, d.n_heads, d.d_c + d.d_r), torch.bfloat16),
+                self._arg(out, "out", (M, d.n_heads, d.d_c), torch.bfloat16),
+                None if lse is None else self._arg(lse, "lse", (M, d.n_heads), torch.float32))
         with self.planner.on_device():
-            N.dsa_decode_step(self.dims, self.rows, self.cache, _vp(q_idx), _vp(q_scale), _vp(w), _vp(q), _vp(out), _vp(lse),
-                              None, _vp(self.idx), *self._args())
+            N.dsa_decode_step(d, self.rows, self.cache, *args, None, _vp(self.idx), *self._args())
         return out, lse
 
     def indices(self):

@@ -277,9 +277,10 @@ class PagedCache:
     """The caches of one layer behind a DevicePlanner: FP8 indexer keys, and the
     latents in bf16 or in packed 4-bit rows.
 
-    workspace_of: the cache of another layer of the same planner, whose workspace (the
-    scores of a step above all: rows x context x 4 bytes) this one then uses.  The
-    layers' calls must run one after the other, and share one status word."""
+    workspace_of: the cache of another layer of the same planner and sizes, whose workspace
+    (the scores of a step above all: rows x context x 4 bytes) this one then uses.  The
+    layers' calls must run one after the other, and share one status word.
+    q_group: as in dsa_rows; above 1 every request must get a multiple of it in each plan."""
 
     def __init__(self, planner: DevicePlanner, n_heads: int = 128, topk: int = 2048, int4: bool = True,
                  sm_scale: float | None = None, q_group: int = 1, workspace_of: "PagedCache | None" = None):
@@ -307,8 +308,9 @@ class PagedCache:
                 N.dsa_workspace_init(_vp(self._ws), nb, p.stream)
             elif workspace_of.planner is not planner:
                 raise ValueError("workspace_of: a layer of another planner")
-            elif workspace_of._ws.numel() < nb:
-                raise ValueError(f"workspace_of: {workspace_of._ws.numel()} bytes, {nb} needed")
+            elif bytes(workspace_of.dims) != bytes(self.dims) or workspace_of.rows.q_group != q_group:
+                # (captured graphs count on what lies where: a step leaves its histograms zero)
+                raise ValueError("workspace_of: a layer of other sizes")
             else:
                 self._ws = workspace_of._ws
 

@@ -61,5 +61,8 @@ def test_refusals():
     small = PagedCache(pl, topk=16)
     with pytest.raises(ValueError, match="another planner"):
         PagedCache(other, topk=16, workspace_of=small)
-    with pytest.raises(ValueError, match="needed"):
-        PagedCache(pl, topk=2048, workspace_of=small)
+    for kw in (dict(topk=2048), dict(topk=8), dict(topk=16, int4=False), dict(topk=16, n_heads=64), dict(topk=16, sm_scale=1.0),
+               dict(topk=16, q_group=2)):
+        with pytest.raises(ValueError, match="other sizes"):
+            PagedCache(pl, workspace_of=small, **kw)
+    assert PagedCache(pl, topk=16, workspace_of=small)._ws is small._ws

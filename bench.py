@@ -198,6 +198,8 @@ def kernel_traffic(kernel: str, workload: str, alg_bytes: int):
             return None
         h.update(open(src, "rb").read())
     if h.hexdigest() != d["sha256"]:
+        print(f"bench: traffic of {kernel}@{workload} left out: its sources changed since profiles/traffic.json was captured",
+              file=sys.stderr)
         return None
     return d["dram_bytes"] * alg_bytes / d["algorithmic_bytes"]
 

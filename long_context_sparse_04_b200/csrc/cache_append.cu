@@ -280,8 +280,9 @@ cache_append_kernel(const AppendArgs a) {
 // 22 us for their 146 MB: what bounds it is the integer pipe (unpacking, packing and
 // comparing; a warp instruction takes it two cycles).  fp32 pairs and bf16 pair maxima
 // took it from 42.4 to 39.2, CTAs of four warps instead of eight to 37.2.  Persistent
-// warps with the next token's loads in flight measured the same; 32 warps an SM, which
-// spill nothing, 41.3.
+// warps with the next token's loads in flight measured the same.  Ten CTAs an SM leave a
+// thread 48 registers, for which it spills 100 bytes and reloads 96; eight CTAs, without
+// a spill (60 registers), took 2 us more, twelve (40 registers) 1 us.
 struct Token {
   float4 key;              // this lane's first key chunk (d_I > 128: the others are loaded late)
   uint4 lat[2], rope;      // its group of 16 dims, its piece of the RoPE key

@@ -8,10 +8,13 @@
 //   latent_out[n] = code * scale per 16 dims, bf16   (exact), RoPE key copied
 //
 // A stream: with 4-bit latents 548 bytes in and 1,664 out per token, so writes
-// bound it.  131,072 tokens take 55.7 us, 5.2 TB/s (a kernel that copies 218 MB of
-// such output alone ran at 5.9).  One warp per token, CTAs of four, fourteen an SM:
-// eight warps a CTA took 57.6 us, sixteen 61.7, two 71; two tokens a warp, persistent
-// warps and a ring filled by cp.async 70-89; 32-byte stores 66.7.
+// bound it.  131,072 tokens take 55.4 us, 5.3 TB/s (a kernel that copies 218 MB of
+// such output alone ran at 5.9); bf16 rows (387 MB) 79.6 us against a floor of 59.2, fp32
+// (739 MB) 122 against 113.  One warp per token, CTAs of four, fourteen an SM, for whose 32
+// registers a thread the compiler spills 28 bytes and reloads 60: ten CTAs, without a spill,
+// took 57.4, twelve 65.5, sixteen the same as fourteen.  Eight warps a CTA took 57.6 us,
+// sixteen 61.7, two 71; two tokens a warp, persistent warps and a ring filled by cp.async
+// 70-89; 32-byte stores 66.7.
 #include <cuda_fp8.h>
 
 #include "dsa_int4.cuh"

@@ -2,10 +2,11 @@
 // group scale and the conversions in both directions.  The format is defined in
 // include/dsa.h.
 //
-// Decoding costs three instructions per pair of dims.  A 4-bit two's complement
-// code q XOR 8 is q + 8, so (nibble ^ 8) placed under the bf16 pattern of 128
-// reads as 136 + q; times the scale S minus 136 S gives q S.  All of it is exact
-// in bf16: S has at most 4 significant bits, 136 S = 17 * 8 * S at most 8
+// Decoding costs three instructions per pair of dims, by a method in common use: a
+// small integer placed under the bits of a floating-point number converts itself.  A
+// 4-bit two's complement code q XOR 8 is q + 8, so (nibble ^ 8) placed under the bf16
+// pattern of 128 reads as 136 + q; times the scale S minus 136 S gives q S.  All of it
+// is exact in bf16: S has at most 4 significant bits, 136 S = 17 * 8 * S at most 8
 // (17 * 15 < 256), and q S at most 8.
 #pragma once
 

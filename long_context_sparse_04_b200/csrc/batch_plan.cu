@@ -340,7 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1) batch_plan_kernel(const __grid_co
     a.p.tok_pos[t] = pos;
     a.p.slot[t] = slot;
   }
-  for (int k = gid; k < (int)taken; k += step) {
+  for (int64_t k64 = gid; k64 < taken; k64 += step) {
+    const int32_t k = (int32_t)k64;
     const int b = owner(pg_start, B, k);
     const int32_t held = pages_of(a.p.seq_len[b], a.page_size);
     a.block_table[(int64_t)b * W + held + (k - pg_start[b])] = taken_page(k);
@@ -348,20 +349,21 @@ __global__ void __launch_bounds__(kThreads, 1) batch_plan_kernel(const __grid_co
   const int64_t left = min(have - taken, (int64_t)a.p.free_capacity);
   // Pages handed back, in runs of kRun * 32 a warp: one search where a run is one request's,
   // and all its loads in flight before its first store.
-  const int32_t back = (int32_t)max(left - F, (int64_t)0);
+  const int64_t back = left - F;
   const auto hand_back = [&](auto run) {
     constexpr int kRun = decltype(run)::value;
-    for (int64_t i64 = (int64_t)(gid >> 5) * (32 * kRun); i64 < back; i64 += (int64_t)step * kRun) {
-      const int32_t i0 = (int32_t)i64, b0 = owner(give_start, B, i0), end = give_start[b0 + 1];
+    for (int64_t i0 = (int64_t)(gid >> 5) * (32 * kRun); i0 < back; i0 += (int64_t)step * kRun) {
+      const int b0 = owner(give_start, B, (int32_t)i0), end = give_start[b0 + 1];
       int32_t page[kRun];
 #pragma unroll
       for (int u = 0; u < kRun; ++u) {
-        const int32_t i = i0 + 32 * u + (tid & 31), b = i < end ? b0 : owner(give_start, B, min(i, back - 1));
+        const int64_t i = i0 + 32 * u + (tid & 31);
+        const int b = i < end ? b0 : owner(give_start, B, (int32_t)min(i, back - 1));
         if (i < back) page[u] = a.block_table[(int64_t)b * W + (i - give_start[b])];
       }
 #pragma unroll
       for (int u = 0; u < kRun; ++u) {
-        const int32_t i = i0 + 32 * u + (tid & 31);
+        const int64_t i = i0 + 32 * u + (tid & 31);
         if (i < back) a.p.free_pages[F + i] = page[u];
       }
     }

@@ -50,12 +50,12 @@
 // Decode batches split a row's keys over 2 or 4 pairs of one cluster, which merge
 // through distributed shared memory: no scratch in global memory, no arrival order.
 //
-// Measured with 128 heads and 2,048 selected keys: 32 rows 30 us (56,000 cycles: 8,000
+// Measured with 128 heads and 2,048 selected keys: 32 rows 32 us (56,000 cycles: 8,000
 // to the first tile, 16 blocks, 12,000 of merge and output) against a floor of 11.1 us
-// of tensor time; 2,048 rows 1.11 ms (1.05 PFLOP/s) on a cool card and 1.25 under its
+// of tensor time; 2,048 rows 1.11 ms (1.05 PFLOP/s) on a cool card and 1.28 under its
 // power cap, floor 0.71.  A block takes about 2,000 cycles: what a decoding group needs
 // for its two tiles of two blocks, waits and arrivals included, at 8 cycles an
-// instruction (issue slots 62 % used, tensor pipe 45 %).
+// instruction (148 rows: issue slots 64 % used, tensor pipe 46 %).
 #include <cudaTypedefs.h>
 
 #include "dsa_int4.cuh"

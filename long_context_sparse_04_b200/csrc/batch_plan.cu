@@ -15,8 +15,10 @@
 // wait for them all the same, and a cluster, which could share them, is 8 CTAs).  200
 // requests of up to 128K tokens in pages of 16 that hand back 239,770 take 24 us with 16
 // CTAs and runs of eight pages a thread, 150 with one CTA, 519 without the runs as well;
-// where nothing is handed back the further CTAs cost 0.2 us.  What bounds it is latency:
-// the launch, two loads in a chain, the scans' barriers, the searches.
+// where nothing is handed back the further CTAs cost 0.2 to 0.4 us.  What bounds a
+// decoding batch is latency: the launch, two loads in a chain, the scans' barriers, the
+// arrival of the CTAs; thousands of requests are bound by what every CTA does for them
+// (half of the time of 4,096).
 // Lengths and the free count, which may be updated in place, are written by the CTA
 // that finishes last, when every CTA has read them; free-list entries read (below the
 // old count) and written (at or above it) never meet, nor do table entries read (pages
